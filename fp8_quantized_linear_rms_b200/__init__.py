@@ -2,7 +2,7 @@
 
 Argument marshalling only: every entry point takes torch CUDA tensors, checks
 dtypes and shapes enough to pass the right pointers, and calls the C ABI of
-``include/fp8q.h`` with the current CUDA stream.  All arithmetic runs in the
+``include/fp8q.h`` and ``include/fp8q_fp4.h`` with the current CUDA stream.  All arithmetic runs in the
 library's kernels; there is no CPU or PyTorch fallback, and importing this
 package fails loudly if ``libfp8q.so`` is missing (build it with
 ``python fp8_quantized_linear_rms_b200/build.py``).
@@ -12,6 +12,10 @@ The names match the C ABI:
                                                                 (activation quant)
   fp8q_scaled_mm, fp8q_scaled_mm_blockwise, fp8q_scaled_mm_blockwise_e8m0,
   fp8q_scaled_mm_blockwise_silu_quant                           (scaled FP8 GEMMs)
+  fp8q_fp4_quant, fp8q_rmsnorm_fp4_quant, fp8q_silu_mul_fp4_quant, fp8q_fp4_dequant,
+  fp8q_scaled_mm_fp4                                            (4-bit nvfp4 / mxfp4)
+  fp8q_moe_route, fp8q_moe_plan, fp8q_moe_fp4_quant, fp8q_grouped_mm_fp4,
+  fp8q_grouped_mm_fp4_silu_quant, fp8q_moe_combine, fp8q_moe_experts_fp4  (experts)
   fp8q_workspace_bytes, fp8q_select_gemm_variant, fp8q_force_gemm_variant,
   fp8q_last_device_status, fp8q_status_string, fp8q_version
 """
@@ -20,12 +24,14 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+from typing import NamedTuple
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfp8q.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp8q.h")
+FP4_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp8q_fp4.h")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libfp8q.so not found at {LIB_PATH}; build it with "
@@ -78,6 +84,24 @@ _SIGS = {
     "fp8q_silu_mul_quant_i8": (_INT, [_P, _I64, _I64, _I64, _INT, _P, _I64, _P, _I64, _I64, _P]),
     "fp8q_scaled_mm_i8": (_INT, [_P, _P, _P, _INT, _P, _INT, _I64, _I64, _I64, _P, _I64, _P,
                                  ctypes.c_size_t, _P]),
+    "fp8q_fp4_sf_bytes": (ctypes.c_size_t, [_I64, _I64, _INT]),
+    "fp8q_fp4_quant": (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _I64, _P, _P]),
+    "fp8q_silu_mul_fp4_quant": (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _I64, _P, _P]),
+    "fp8q_rmsnorm_fp4_quant": (_INT, [_P, _P, ctypes.c_float, _I64, _I64, _I64, _INT, _P, _P, _I64, _P, _P]),
+    "fp8q_fp4_dequant": (_INT, [_P, _I64, _P, _INT, _P, _I64, _I64, _P, _I64, _P]),
+    "fp8q_scaled_mm_fp4": (_INT, [_P, _P, _P, _P, _INT, _P, _P, _I64, _I64, _I64, _P, _I64, _P]),
+    "fp8q_moe_route": (_INT, [_P, _INT, _I64, _I64, _I64, _INT, _INT, _P, _INT, _INT, _INT, ctypes.c_float,
+                              _P, _P, _P]),
+    "fp8q_moe_plan_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "fp8q_moe_plan": (_INT, [_P, _I64, _I64, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "fp8q_moe_fp4_quant": (_INT, [_P, _I64, _I64, _I64, _INT, _P, _P, _INT, _P, _P, _I64, _P, _P]),
+    "fp8q_grouped_mm_fp4": (_INT, [_P, _P, _P, _P, _INT, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _I64, _P]),
+    "fp8q_grouped_mm_fp4_silu_quant": (_INT, [_P, _P, _P, _P, _INT, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P,
+                                              _P, _P, _P]),
+    "fp8q_moe_combine": (_INT, [_P, _I64, _P, _P, _I64, _INT, _I64, _P, _I64, _P]),
+    "fp8q_moe_experts_fp4_workspace_bytes": (ctypes.c_size_t, [_I64, _INT, _I64, _I64, _I64, _INT]),
+    "fp8q_moe_experts_fp4": (_INT, [_P, _I64, _I64, _P, _P, _INT, _I64, _I64, _I64, _INT, _P, _P, _P, _P, _P, _P,
+                                    _P, _P, _P, _I64, _P, ctypes.c_size_t, _P]),
     "fp8q_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _INT]),
     "fp8q_select_gemm_variant": (_INT, [_I64, _I64, _I64, _INT, ctypes.POINTER(GemmVariant)]),
     "fp8q_force_gemm_variant": (_INT, [ctypes.POINTER(GemmVariant)]),
@@ -97,9 +121,9 @@ class Fp8qError(RuntimeError):
         super().__init__(f"{fn} failed: {lib.fp8q_status_string(status).decode()} ({status})")
 
 
-def header_functions() -> list[str]:
-    """Names of every function include/fp8q.h declares."""
-    with open(HEADER_PATH) as f:
+def header_functions(path: str = HEADER_PATH) -> list[str]:
+    """Names of every function include/fp8q.h (or the header at `path`) declares."""
+    with open(path) as f:
         text = f.read()
     return re.findall(r"^FP8Q_API\s+[\w\s\*]+?\b(fp8q_\w+)\s*\(", text, flags=re.M)
 
@@ -506,6 +530,405 @@ def fp8q_scaled_mm_i8(a_q: torch.Tensor, b_q: torch.Tensor, a_scale: torch.Tenso
         b_scale.data_ptr(), int(b_scale.numel() == N), M, N, K, y.data_ptr(), _rowmajor(y, "y"), wp,
         wn, _stream(stream)))
     return y
+
+
+# --------------------------------------------------------------- 4-bit microscaled operands
+_FP4_FORMATS = {"nvfp4": (0, 16), "mxfp4": (1, 32)}
+
+
+def _fp4(fmt: str):
+    """"nvfp4" / "mxfp4" -> (the ABI's format, values in a group)."""
+    try:
+        return _FP4_FORMATS[fmt]
+    except (KeyError, TypeError):
+        raise ValueError(f"format must be 'nvfp4' or 'mxfp4', got {fmt!r}") from None
+
+
+def _launch_stream(stream, first: torch.Tensor, *rest) -> int | None:
+    """The raw stream to launch on; every tensor must be on the current device
+    (the kernels, and the outputs allocated for them, go there)."""
+    dev = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def _torch_stream(stream):
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+
+
+def _empty(shape, dtype, like: torch.Tensor, stream):
+    """A tensor that belongs to the stream the kernels run on, so that its
+    memory is not handed on while they still use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _gscale(t, n: int, name: str):
+    if t is None:
+        return None
+    _need(t, torch.float32, name)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous value(s)")
+    return t.data_ptr()
+
+
+def _sf_shape(rows: int, K: int, group: int):
+    return (-(-rows // 128), -(-K // (4 * group)), 512)
+
+
+def _need_sf(sf, rows: int, K: int, group: int, name: str, lead: int | None = None) -> int:
+    _need(sf, torch.uint8, name)
+    shape = _sf_shape(rows, K, group)
+    want = shape if lead is None else (lead, *shape)
+    if sf.numel() != shape[0] * shape[1] * 512 * (1 if lead is None else lead) or not sf.is_contiguous():
+        raise ValueError(f"{name} must be contiguous scale blocks {want}, got {tuple(sf.shape)}")
+    return sf.data_ptr()
+
+
+def _need_codes(q, name: str, dims: int = 2) -> None:
+    _need(q, torch.uint8, name)
+    if q.dim() != dims or not q.is_contiguous():
+        raise ValueError(f"{name} must be contiguous packed codes with {dims} dimensions")
+
+
+def fp4_sf_shape(rows: int, K: int, fmt: str):
+    """Shape of the uint8 scale blocks of a [rows, K] matrix: [ceil(rows / 128),
+    ceil(groups / 4), 512]; the scale of row r and group j is byte
+    (r % 32) * 16 + (r % 128) // 32 * 4 + j % 4 of block [r // 128, j // 4]."""
+    return _sf_shape(rows, K, _fp4(fmt)[1])
+
+
+def _fp4_quant_out(M, K, group, x, q, sf, stream):
+    if q is None:
+        q = _empty((M, K // 2), torch.uint8, x, stream)
+    else:
+        _need(q, torch.uint8, "q")
+        if tuple(q.shape) != (M, K // 2):
+            raise ValueError(f"q must be [{M}, {K // 2}]")
+    if sf is None:
+        sf = _empty(_sf_shape(M, K, group), torch.uint8, x, stream)
+    return q, _rowmajor(q, "q"), sf, _need_sf(sf, M, K, group, "sf")
+
+
+def fp8q_fp4_quant(x: torch.Tensor, fmt: str, gscale=None, q=None, sf=None, stream=None):
+    """4-bit quantization of bf16 rows [M, K] (K a multiple of 32).  Returns (q uint8 [M, K/2],
+    two e2m1 codes a byte; sf uint8 scale blocks of fp4_sf_shape).  fmt "nvfp4": groups of 16,
+    e4m3 scales, value = code * scale * gscale (fp32 [1] on the device, or None); "mxfp4": groups
+    of 32, E8M0 scales.  Also quantizes weights (a row is an output channel)."""
+    _need(x, torch.bfloat16, "x")
+    ldx = _rowmajor(x, "x")
+    f, group = _fp4(fmt)
+    M, K = x.shape
+    g = _gscale(gscale, 1, "gscale")
+    q, ldq, sf, sp = _fp4_quant_out(M, K, group, x, q, sf, stream)
+    st = lib.fp8q_fp4_quant(x.data_ptr(), M, K, ldx, f, g, q.data_ptr(), ldq, sp,
+                            _launch_stream(stream, x, q, sf, gscale))
+    _check("fp8q_fp4_quant", st)
+    return q, sf
+
+
+def fp8q_rmsnorm_fp4_quant(x: torch.Tensor, w: torch.Tensor, eps: float, fmt: str, gscale=None, q=None,
+                           sf=None, stream=None):
+    """RMSNorm + 4-bit quantization; outputs as in fp8q_fp4_quant."""
+    _need(x, torch.bfloat16, "x")
+    _need(w, torch.bfloat16, "w")
+    ldx = _rowmajor(x, "x")
+    f, group = _fp4(fmt)
+    M, H = x.shape
+    if w.numel() != H or not w.is_contiguous():
+        raise ValueError(f"w must hold {H} contiguous values")
+    g = _gscale(gscale, 1, "gscale")
+    q, ldq, sf, sp = _fp4_quant_out(M, H, group, x, q, sf, stream)
+    st = lib.fp8q_rmsnorm_fp4_quant(x.data_ptr(), w.data_ptr(), eps, M, H, ldx, f, g, q.data_ptr(), ldq, sp,
+                                    _launch_stream(stream, x, w, q, sf, gscale))
+    _check("fp8q_rmsnorm_fp4_quant", st)
+    return q, sf
+
+
+def fp8q_silu_mul_fp4_quant(x: torch.Tensor, fmt: str, gscale=None, q=None, sf=None, stream=None):
+    """SiLU*mul + 4-bit quantization of x [M, 2I] = [gate | up]; outputs [M, I] as in fp8q_fp4_quant."""
+    _need(x, torch.bfloat16, "x")
+    ldx = _rowmajor(x, "x")
+    f, group = _fp4(fmt)
+    M, I2 = x.shape
+    if I2 % 2:
+        raise ValueError("x must have an even number of columns")
+    I = I2 // 2
+    g = _gscale(gscale, 1, "gscale")
+    q, ldq, sf, sp = _fp4_quant_out(M, I, group, x, q, sf, stream)
+    st = lib.fp8q_silu_mul_fp4_quant(x.data_ptr(), M, I, ldx, f, g, q.data_ptr(), ldq, sp,
+                                     _launch_stream(stream, x, q, sf, gscale))
+    _check("fp8q_silu_mul_fp4_quant", st)
+    return q, sf
+
+
+def fp8q_fp4_dequant(q: torch.Tensor, sf: torch.Tensor, fmt: str, gscale=None, y=None, stream=None):
+    """bf16 values [M, K] of packed codes q [M, K/2] and their scale blocks."""
+    _need(q, torch.uint8, "q")
+    ldq = _rowmajor(q, "q")
+    f, group = _fp4(fmt)
+    M, K = q.shape[0], 2 * q.shape[1]
+    sp = _need_sf(sf, M, K, group, "sf")
+    g = _gscale(gscale, 1, "gscale")
+    y = _y_out(y, M, K, q, stream)
+    st = lib.fp8q_fp4_dequant(q.data_ptr(), ldq, sp, f, g, M, K, y.data_ptr(), _rowmajor(y, "y"),
+                              _launch_stream(stream, q, sf, gscale, y))
+    _check("fp8q_fp4_dequant", st)
+    return y
+
+
+def _y_out(y, M, N, like, stream):
+    if y is None:
+        return _empty((M, N), torch.bfloat16, like, stream)
+    _need(y, torch.bfloat16, "y")
+    if tuple(y.shape) != (M, N):
+        raise ValueError(f"y must be [{M}, {N}]")
+    return y
+
+
+def fp8q_scaled_mm_fp4(a_q: torch.Tensor, b_q: torch.Tensor, a_sf: torch.Tensor, b_sf: torch.Tensor, fmt: str,
+                       a_gscale=None, b_gscale=None, y=None, stream=None):
+    """Block-scaled GEMM on 4-bit operands: y [M, N] bf16 of codes a_q [M, K/2], b_q [N, K/2] and
+    their scale blocks (and fp32 [1] tensor scales); N a multiple of 16.  The tensor core applies
+    the scales."""
+    _need_codes(a_q, "a_q")
+    _need_codes(b_q, "b_q")
+    f, group = _fp4(fmt)
+    (M, K2), N = a_q.shape, b_q.shape[0]
+    if b_q.shape[1] != K2:
+        raise ValueError("a_q and b_q must have the same depth")
+    ap = _need_sf(a_sf, M, 2 * K2, group, "a_sf")
+    bp = _need_sf(b_sf, N, 2 * K2, group, "b_sf")
+    ga, gb = _gscale(a_gscale, 1, "a_gscale"), _gscale(b_gscale, 1, "b_gscale")
+    y = _y_out(y, M, N, a_q, stream)
+    st = lib.fp8q_scaled_mm_fp4(a_q.data_ptr(), b_q.data_ptr(), ap, bp, f, ga, gb, M, N, 2 * K2, y.data_ptr(),
+                                _rowmajor(y, "y"),
+                                _launch_stream(stream, a_q, b_q, a_sf, b_sf, a_gscale, b_gscale, y))
+    _check("fp8q_scaled_mm_fp4", st)
+    return y
+
+
+# --------------------------------------------------------------- experts
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def fp8q_moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", bias=None, num_groups: int = 1,
+                   topk_groups: int = 1, renormalize: bool = True, scale: float = 1.0, weights=None, ids=None,
+                   stream=None):
+    """Experts of each token from router logits [T, E] (fp32 or bf16).  Scores are a softmax over
+    the experts or a sigmoid of each; `bias` (fp32 [E]) is added for the selection only; with
+    topk_groups < num_groups only experts of the best groups of neighbours are selected (a group
+    counts with its largest key, with a bias the sum of its two largest).  Equal keys go to the
+    lowest index; -inf or NaN logits mask.  Returns (weights fp32 [T, top_k], ids int32 [T, top_k])
+    in descending order of the key; weights are scores, divided by their sum if `renormalize`,
+    times `scale`."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if scoring not in _SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
+    ld = _rowmajor(logits, "logits")
+    T, E = logits.shape
+    if bias is not None:
+        _gscale(bias, E, "bias")
+    if weights is None:
+        weights = _empty((T, top_k), torch.float32, logits, stream)
+    if ids is None:
+        ids = _empty((T, top_k), torch.int32, logits, stream)
+    _need_entries(weights, torch.float32, T, top_k, "weights")
+    _need_entries(ids, torch.int32, T, top_k, "ids")
+    st = lib.fp8q_moe_route(logits.data_ptr(), logits.dtype is torch.bfloat16, T, E, ld if T > 1 else max(ld, E),
+                            top_k, _SCORING[scoring], None if bias is None else bias.data_ptr(), num_groups,
+                            topk_groups, bool(renormalize), scale, weights.data_ptr(), ids.data_ptr(),
+                            _launch_stream(stream, logits, bias, weights, ids))
+    _check("fp8q_moe_route", st)
+    return weights, ids
+
+
+def _need_entries(t, dtype, T, k, name):
+    _need(t, dtype, name)
+    if tuple(t.shape) != (T, k) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{T}, {k}]")
+
+
+class MoePlan(NamedTuple):
+    """What fp8q_moe_plan returns: int32 tensors."""
+    offsets: torch.Tensor      # [E + 1] first row of each expert
+    sf_offsets: torch.Tensor   # [E + 1] first block row of each expert's scales
+    pos: torch.Tensor          # [T, top_k] an entry's row, or -1
+    sf_row: torch.Tensor       # [T, top_k] the row whose place its scales take, or -1
+
+
+def fp8q_moe_plan(ids: torch.Tensor, num_experts: int, stream=None) -> MoePlan:
+    """Rows of the (token, slot) entries of ids int32 [T, top_k], ordered by expert, in entry order
+    within an expert; ids outside [0, num_experts) get none."""
+    _need(ids, torch.int32, "ids")
+    if ids.dim() != 2 or not ids.is_contiguous():
+        raise ValueError("ids must be contiguous [T, top_k]")
+    n = ids.numel()
+    offsets, sf_offsets = (_empty((num_experts + 1,), torch.int32, ids, stream) for _ in range(2))
+    pos, sf_row = (_empty(ids.shape, torch.int32, ids, stream) for _ in range(2))
+    nws = lib.fp8q_moe_plan_workspace_bytes(n, num_experts)
+    ws = _empty((nws,), torch.uint8, ids, stream) if nws else None
+    st = lib.fp8q_moe_plan(ids.data_ptr(), n, num_experts, offsets.data_ptr(), sf_offsets.data_ptr(),
+                           pos.data_ptr(), sf_row.data_ptr(), None if ws is None else ws.data_ptr(), nws,
+                           _launch_stream(stream, ids))
+    _check("fp8q_moe_plan", st)
+    return MoePlan(offsets, sf_offsets, pos, sf_row)
+
+
+def moe_sf_rows(n: int, num_experts: int) -> int:
+    """Rows of scale blocks that n rows of the experts may take: every expert's begin a block row."""
+    return 128 * (n // 128 + min(n, num_experts))
+
+
+def fp8q_moe_fp4_quant(x: torch.Tensor, plan: MoePlan, fmt: str, gscale=None, stream=None):
+    """fp8q_fp4_quant of tokens [T, H], each written to the rows of its experts.  Returns
+    (q [T * top_k, H/2], sf) as fp8q_grouped_mm_fp4 reads them."""
+    _need(x, torch.bfloat16, "x")
+    ldx = _rowmajor(x, "x")
+    f, group = _fp4(fmt)
+    T, K = x.shape
+    _need_entries(plan.pos, torch.int32, T, plan.pos.shape[1], "plan.pos")
+    _need_entries(plan.sf_row, torch.int32, T, plan.pos.shape[1], "plan.sf_row")
+    n = plan.pos.numel()
+    g = _gscale(gscale, 1, "gscale")
+    q = _empty((n, K // 2), torch.uint8, x, stream)
+    sf = _empty(_sf_shape(moe_sf_rows(n, plan.offsets.numel() - 1), K, group), torch.uint8, x, stream)
+    st = lib.fp8q_moe_fp4_quant(x.data_ptr(), T, K, ldx, plan.pos.shape[1], plan.pos.data_ptr(),
+                                plan.sf_row.data_ptr(), f, g, q.data_ptr(), K // 2, sf.data_ptr(),
+                                _launch_stream(stream, x, gscale, *plan))
+    _check("fp8q_moe_fp4_quant", st)
+    return q, sf
+
+
+def _grouped(a_q, b_q, a_sf, b_sf, fmt, plan, a_gscale, b_gscale):
+    _need_codes(a_q, "a_q")
+    _need_codes(b_q, "b_q", 3)
+    f, group = _fp4(fmt)
+    (M, K2), (E, N, Kb) = a_q.shape, b_q.shape
+    if Kb != K2:
+        raise ValueError("a_q and b_q must have the same depth")
+    for t, name in ((plan.offsets, "plan.offsets"), (plan.sf_offsets, "plan.sf_offsets")):
+        _need(t, torch.int32, name)
+        if t.numel() != E + 1 or not t.is_contiguous():
+            raise ValueError(f"{name} must hold {E + 1} contiguous values")
+    if plan.pos.numel() != M:
+        raise ValueError(f"a_q has {M} rows, the plan {plan.pos.numel()} entries")
+    _need_sf(a_sf, moe_sf_rows(M, E), 2 * K2, group, "a_sf")
+    _need_sf(b_sf, N, 2 * K2, group, "b_sf", E)
+    return f, group, M, N, 2 * K2, E, _gscale(a_gscale, 1, "a_gscale"), _gscale(b_gscale, E, "b_gscale")
+
+
+def fp8q_grouped_mm_fp4(a_q: torch.Tensor, b_q: torch.Tensor, a_sf: torch.Tensor, b_sf: torch.Tensor, fmt: str,
+                        plan: MoePlan, a_gscale=None, b_gscale=None, y=None, stream=None):
+    """Each expert's rows times its weights: y [M, N] bf16 from a_q [M, K/2] and a_sf (rows as the
+    plan orders them), b_q [E, N, K/2] and b_sf [E, *fp4_sf_shape(N, K, fmt)]; a_gscale fp32 [1],
+    b_gscale fp32 [E].  Rows without an expert are not written."""
+    f, group, M, N, K, E, ga, gb = _grouped(a_q, b_q, a_sf, b_sf, fmt, plan, a_gscale, b_gscale)
+    y = _y_out(y, M, N, a_q, stream)
+    st = lib.fp8q_grouped_mm_fp4(a_q.data_ptr(), b_q.data_ptr(), a_sf.data_ptr(), b_sf.data_ptr(), f, ga, gb,
+                                 plan.offsets.data_ptr(), plan.sf_offsets.data_ptr(), E, M, N, K, y.data_ptr(),
+                                 _rowmajor(y, "y"),
+                                 _launch_stream(stream, a_q, b_q, a_sf, b_sf, a_gscale, b_gscale, y, *plan))
+    _check("fp8q_grouped_mm_fp4", st)
+    return y
+
+
+def fp8q_grouped_mm_fp4_silu_quant(a_q: torch.Tensor, b_q: torch.Tensor, a_sf: torch.Tensor, b_sf: torch.Tensor,
+                                   fmt: str, plan: MoePlan, a_gscale=None, b_gscale=None, gscale=None, stream=None):
+    """The experts' gate_up product with SiLU*mul and the next quantization in its epilogue: b_q
+    [E, 2I, K/2] = [gate | up] rows, I a multiple of 128.  Returns (q [M, I/2], sf) at the plan's
+    rows, with tensor scale `gscale`."""
+    f, group, M, N, K, E, ga, gb = _grouped(a_q, b_q, a_sf, b_sf, fmt, plan, a_gscale, b_gscale)
+    g = _gscale(gscale, 1, "gscale")
+    I = N // 2
+    q = _empty((M, I // 2), torch.uint8, a_q, stream)
+    sf = _empty(_sf_shape(moe_sf_rows(M, E), I, group), torch.uint8, a_q, stream)
+    st = lib.fp8q_grouped_mm_fp4_silu_quant(
+        a_q.data_ptr(), b_q.data_ptr(), a_sf.data_ptr(), b_sf.data_ptr(), f, ga, gb, plan.offsets.data_ptr(),
+        plan.sf_offsets.data_ptr(), E, M, I, K, g, q.data_ptr(), sf.data_ptr(),
+        _launch_stream(stream, a_q, b_q, a_sf, b_sf, a_gscale, b_gscale, gscale, *plan))
+    _check("fp8q_grouped_mm_fp4_silu_quant", st)
+    return q, sf
+
+
+def fp8q_moe_combine(o: torch.Tensor, plan: MoePlan, weights: torch.Tensor, y=None, stream=None):
+    """y [T, H] bf16 = the sum over slots of weights [T, top_k] times rows plan.pos of o (bf16)."""
+    _need(o, torch.bfloat16, "o")
+    T, k = plan.pos.shape
+    _need_entries(plan.pos, torch.int32, T, k, "plan.pos")
+    _need_entries(weights, torch.float32, T, k, "weights")
+    if o.shape[0] != T * k:
+        raise ValueError(f"o must have {T * k} rows")
+    H = o.shape[1]
+    y = _y_out(y, T, H, o, stream)
+    st = lib.fp8q_moe_combine(o.data_ptr(), _rowmajor(o, "o"), plan.pos.data_ptr(), weights.data_ptr(), T, k, H,
+                              y.data_ptr(), _rowmajor(y, "y"), _launch_stream(stream, o, weights, y, plan.pos))
+    _check("fp8q_moe_combine", st)
+    return y
+
+
+def make_moe_workspace(T: int, top_k: int, num_experts: int, H: int, I: int, fmt: str, device="cuda"):
+    """A workspace for fp8q_moe_experts_fp4 of up to T tokens (any content)."""
+    n = lib.fp8q_moe_experts_fp4_workspace_bytes(T, top_k, num_experts, H, I, _fp4(fmt)[0])
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor,
+                         w13_sf: torch.Tensor, w2: torch.Tensor, w2_sf: torch.Tensor, fmt: str, x_gscale=None,
+                         w13_gscale=None, h_gscale=None, w2_gscale=None, y=None, workspace=None, stream=None):
+    """The experts' pass over tokens x bf16 [T, H]: y[t] = sum_j weights[t, j] W2_e quant(silu(gate) up),
+    e = ids[t, j].  w13 codes [E, 2I, H/2] = [gate | up], w2 codes [E, H, I/2], with scale blocks
+    [E, *fp4_sf_shape(rows, cols, fmt)]; x_gscale, h_gscale fp32 [1], w13_gscale, w2_gscale fp32 [E].
+    Six launches at most; ids outside [0, E) add nothing."""
+    _need(x, torch.bfloat16, "x")
+    ldx = _rowmajor(x, "x")
+    _need_codes(w13, "w13", 3)
+    _need_codes(w2, "w2", 3)
+    f, group = _fp4(fmt)
+    (T, H), (E, I2, Hh) = x.shape, w13.shape
+    I = I2 // 2
+    if Hh * 2 != H or I2 % 2 or tuple(w2.shape) != (E, H, I // 2):
+        raise ValueError(f"x {tuple(x.shape)}, w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit")
+    k = ids.shape[-1]
+    _need_entries(ids, torch.int32, T, k, "ids")
+    _need_entries(weights, torch.float32, T, k, "weights")
+    s13, s2 = _need_sf(w13_sf, I2, H, group, "w13_sf", E), _need_sf(w2_sf, H, I, group, "w2_sf", E)
+    gx, gh = _gscale(x_gscale, 1, "x_gscale"), _gscale(h_gscale, 1, "h_gscale")
+    g13, g2 = _gscale(w13_gscale, E, "w13_gscale"), _gscale(w2_gscale, E, "w2_gscale")
+    y = _y_out(y, T, H, x, stream)
+    if workspace is None:
+        n = lib.fp8q_moe_experts_fp4_workspace_bytes(T, k, E, H, I, f)
+        workspace = _empty((n,), torch.uint8, x, stream)
+    else:
+        _need(workspace, torch.uint8, "workspace")
+    st = lib.fp8q_moe_experts_fp4(
+        x.data_ptr(), T, ldx, ids.data_ptr(), weights.data_ptr(), k, E, H, I, f, w13.data_ptr(), s13, w2.data_ptr(),
+        s2, gx, g13, gh, g2, y.data_ptr(), _rowmajor(y, "y"), workspace.data_ptr(), workspace.numel(),
+        _launch_stream(stream, x, ids, weights, w13, w13_sf, w2, w2_sf, x_gscale, w13_gscale, h_gscale, w2_gscale, y,
+                       workspace))
+    _check("fp8q_moe_experts_fp4", st)
+    return y
+
+
+def fp8q_fp4_sf_bytes(rows: int, K: int, fmt: str) -> int:
+    return int(lib.fp8q_fp4_sf_bytes(rows, K, _fp4(fmt)[0]))
+
+
+def fp8q_moe_plan_workspace_bytes(n: int, num_experts: int) -> int:
+    return int(lib.fp8q_moe_plan_workspace_bytes(n, num_experts))
+
+
+def fp8q_moe_experts_fp4_workspace_bytes(T: int, top_k: int, num_experts: int, H: int, I: int, fmt: str) -> int:
+    return int(lib.fp8q_moe_experts_fp4_workspace_bytes(T, top_k, num_experts, H, I, _fp4(fmt)[0]))
 
 
 def fp8q_select_gemm_variant(M: int, N: int, K: int, blockwise: bool) -> dict:

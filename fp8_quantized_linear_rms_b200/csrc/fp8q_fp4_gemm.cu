@@ -1,0 +1,627 @@
+// fp8q_fp4_gemm.cu -- block-scaled products of 4-bit microscaled operands
+// (nvfp4, mxfp4) on the tensor cores, dense and grouped by expert, bf16 out or
+// with the experts' SiLU*mul and its requantization in the epilogue.
+//
+//   y[m, n] = bf16_rn( ga gb sum_k (qa[m, k] sfa[m, k/g]) (qb[n, k] sfb[n, k/g]) )
+//
+// The tensor core applies the scales (tcgen05.mma kind::mxf4nvf4 with four
+// e4m3 scales per 64-deep K slice, kind::mxf4 with two E8M0), so the fp32
+// accumulator stays in tensor memory for the whole K range.  Persistent CTAs,
+// warp-specialized as in the FP8 GEMMs: warp 0 feeds a ring of stages (256
+// codes = 128 bytes of every operand row, 128-byte swizzle by TMA, and the
+// matching 512-byte scale blocks by plain bulk copies, which is why scales are
+// stored in blocks), warp 1 copies a stage's scale blocks into tensor memory
+// (tcgen05.cp) and issues its MMAs, the other warps are the epilogue.
+//
+// Tokens sit in the MMA's 128 rows, weights in its BN columns, at every size.
+// A tile of few tokens copies only the 16- or 32-row pieces that hold some;
+// the MMA then computes rows that nobody reads, at no cost where the time is
+// that of reading the weights.  Few tokens take 64 weight rows a tile (the
+// narrowest that may begin inside a 128-row scale block: a 64-column MMA finds
+// its scales two tensor memory columns further), so that a layer spreads over
+// the SMs, two CTAs each; many take 256.
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "fp8q_common.cuh"
+#include "fp8q_fp4_math.cuh"
+#include "fp8q_sm100.cuh"
+
+namespace fp8q {
+namespace {
+
+using namespace sm100;
+
+constexpr int kStageBytes = 128;          // of an operand row: 256 codes
+constexpr int kMaxExperts = 512;
+
+struct Fp4Args {
+  int64_t M, N, K;             // tokens (rows of all experts), weight rows of an expert, depth
+  const uint8_t* sft;          // token scale blocks
+  const uint8_t* sfw;          // weight scale blocks
+  int kb;                      // scale blocks in a block row
+  int kstages;                 // 256-deep steps
+  int64_t wblocks;             // block rows of an expert's weight scales
+  const float* ga;             // scale of the tokens' tensor (1 value) or null
+  const float* gb;             // scales of the weights (one an expert) or null
+  uint16_t* y;                 // bf16 [M, N] (not FUSED)
+  int64_t ldy;
+  const int* offsets;          // [E + 1] first row of each expert; null: dense
+  const int* sf_offsets;       // [E + 1] first scale block row of each expert
+  int E;
+  uint8_t* hq;                 // FUSED: codes [M, I / 2], scale blocks, their tensor scale
+  uint8_t* hsf;
+  const float* gh;
+  int64_t I;
+  int tiles_n;                 // weight tiles of an expert
+  int box;                     // token rows of one copy (16, 32, 128)
+  int stages;
+  int a_bytes;                 // shared memory of a stage's token tile
+  int vec32;                   // y may be written 32 bytes at a time
+  int* status;
+};
+
+// D[tmem] (+)= (A SFA)(B SFB)^T, both e2m1.
+template <int FMT>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                        uint32_t sfa, uint32_t sfb) {
+  if constexpr (FMT == kNv) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::
+            "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::
+            "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
+        : "memory");
+  }
+}
+
+// Instruction descriptor of the 4-bit block-scaled kinds: scale id of B (bits
+// 4-5) and A (29-30), e2m1 operands (bits 7-9 and 10-12 = 1), K-major, N >> 3
+// at bits 17-22, scale format (bit 23: 0 e4m3, 1 E8M0), M >> 7 at bits 27-28.
+__device__ __forceinline__ uint32_t idesc_fp4(int fmt, int M, int N, uint32_t id) {
+  return (id << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(fmt == kMx) << 23) | (static_cast<uint32_t>(M >> 7) << 27) | (id << 29);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A tile: its expert, first token row and how many rows are the expert's, the
+// token scales' block row, and the first weight row (of the expert).
+struct Fp4Tile {
+  int e;
+  int64_t t0;
+  int cnt;
+  int64_t tblk;
+  int64_t n0;
+};
+
+// Tile u: an expert's tiles are consecutive, its token tiles the fastest index
+// (they share the weight tile, which then comes from L2).  pre[e]: token tiles
+// before expert e.
+__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const int* pre, int u, int tn) {
+  Fp4Tile t;
+  int lo = 0, hi = p.E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (static_cast<int64_t>(pre[mid]) * p.tiles_n <= u) lo = mid; else hi = mid;
+  }
+  const int mt = pre[lo + 1] - pre[lo];
+  const int r = u - pre[lo] * p.tiles_n;
+  const int nt = r / mt, m = r - nt * mt;
+  const int64_t first = p.offsets ? p.offsets[lo] : 0;
+  const int64_t end = p.offsets ? p.offsets[lo + 1] : p.M;
+  t.e = lo;
+  t.t0 = first + 128 * m;
+  t.cnt = static_cast<int>(min(static_cast<int64_t>(128), end - t.t0));
+  t.tblk = (p.sf_offsets ? p.sf_offsets[lo] : 0) + m;
+  t.n0 = static_cast<int64_t>(nt) * tn;
+  return t;
+}
+
+// ------------------------------------------------------------------- kernel
+// CH output columns a tile: 64, 128 or 256 weight rows, or FUSED 64 or 128
+// hidden channels, whose gate rows are followed by the up rows.  128 channels
+// are one 256-column MMA, 64 are two 64-column ones (gate, up), each with the
+// scale block that its rows lie in.
+template <int FMT, int CH, bool FUSED>
+struct Fp4Cfg {
+  static constexpr bool SMALL = CH == 64;                   // two CTAs on an SM
+  static constexpr int BN = FUSED ? 2 * CH : CH;            // accumulator columns
+  static constexpr bool TWO_MMA = FUSED && SMALL;
+  static constexpr int MMA_N = TWO_MMA ? CH : BN;
+  static constexpr int EPI_WARPS = SMALL && !FUSED ? 4 : 8;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int NKB = FMT == kNv ? 4 : 2;            // scale blocks of a stage, per 128 rows
+  static constexpr int SF_BYTES = NKB * 512;                // per 128 rows
+  static constexpr int SF_COLS = NKB * 4;
+  static constexpr int BBLK = FUSED || BN == 256 ? 2 : 1;   // 128-row blocks of weight scales
+  static constexpr int BBOX = FUSED ? CH : (BN < 128 ? BN : 128);   // weight rows of one copy
+  static constexpr int B_BYTES = BN * kStageBytes;
+  static constexpr int SF_STAGE = (1 + BBLK) * SF_BYTES;
+  static constexpr int SF_TMEM = (1 + BBLK) * SF_COLS;      // tensor memory columns of a stage's scales
+  static constexpr int SFBUF = SMALL ? 2 : 4;
+  static constexpr int NBUF = BN == 256 || TWO_MMA ? 1 : 2; // accumulator buffers
+  static constexpr int ACC_COLS = NBUF * BN;
+  static constexpr int TMEM = SMALL ? 256 : 512;
+  static constexpr int B_STEP = TWO_MMA ? 4 : 4 * BBLK;     // scale columns from one K block to the next
+  static_assert(ACC_COLS + SFBUF * SF_TMEM + 4 <= TMEM, "tensor memory");
+};
+
+template <int FMT, int CH, bool FUSED>
+__global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, CH, FUSED>::SMALL ? 2 : 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmW,
+                    const Fp4Args p) {
+  using C = Fp4Cfg<FMT, CH, FUSED>;
+  constexpr int BN = C::BN, NB = C::NBUF;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int pre[kMaxExperts + 1];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int S = p.stages;
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + S * p.a_bytes;
+  uint8_t* sSF = sB + S * C::B_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sSF + S * C::SF_STAGE);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < NB; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], C::EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tmT);
+    prefetch_tmap(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM);
+    tmem_relinquish();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // pre[e]: token tiles before expert e
+  if (p.offsets == nullptr) {
+    if (threadIdx.x == 0) {
+      pre[0] = 0;
+      pre[1] = static_cast<int>((p.M + 127) / 128);
+    }
+  } else {
+    for (int e = threadIdx.x; e < p.E; e += C::THREADS)
+      pre[e + 1] = (p.offsets[e + 1] - p.offsets[e] + 127) / 128;
+    if (threadIdx.x == 0) pre[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+      int carry = 0;
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane;
+        int v = e < p.E ? pre[e + 1] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+          if (lane >= o) v += w;
+        }
+        if (e < p.E) pre[e + 1] = carry + v;
+        carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int units = pre[p.E] * p.tiles_n;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const Fp4Tile t = fp4_tile(p, pre, u, CH);
+        const int wrow = static_cast<int>(t.e * p.N + t.n0);
+        const int up = FUSED ? static_cast<int>(p.I) : 128;       // from the first copy's rows to the second's
+        const int pieces = (t.cnt + p.box - 1) / p.box;
+        const uint8_t* sft = p.sft + t.tblk * p.kb * 512;
+        const uint8_t* sfw = p.sfw + (t.e * p.wblocks + (t.n0 >> 7)) * p.kb * 512;
+        // a second block of weight scales: the up half's, or columns 128..255
+        const int64_t second = static_cast<int64_t>(up >> 7) * p.kb * 512;
+        const bool two = FUSED || (BN == 256 && t.n0 + 128 < p.N);
+        for (int kb = 0; kb < p.kstages; ++kb, ++it) {
+          const int st = it % S;
+          if (!mbar_wait(&empty[st], ((it / S) & 1) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+          const uint32_t sfb = min(C::NKB, p.kb - kb * C::NKB) * 512;
+          const int64_t sfo = static_cast<int64_t>(kb) * C::SF_BYTES;
+          mbar_arrive_expect_tx(&full[st], pieces * p.box * kStageBytes + C::B_BYTES + (two ? 3 : 2) * sfb);
+          uint8_t* a = sA + st * p.a_bytes;
+          uint8_t* b = sB + st * C::B_BYTES;
+          uint8_t* s = sSF + st * C::SF_STAGE;
+          const int x = kb * kStageBytes;
+          tma_load_2d(b, &tmW, &full[st], x, wrow);
+          if (C::BBLK == 2) tma_load_2d(b + C::BBOX * kStageBytes, &tmW, &full[st], x, wrow + up);
+          bulk_load(s + C::SF_BYTES, sfw + sfo, sfb, &full[st]);
+          if (two) bulk_load(s + 2 * C::SF_BYTES, sfw + second + sfo, sfb, &full[st]);
+          for (int i = 0; i < pieces; ++i)
+            tma_load_2d(a + i * p.box * kStageBytes, &tmT, &full[st], x, static_cast<int>(t.t0) + i * p.box);
+          bulk_load(s, sft + sfo, sfb, &full[st]);
+        }
+      }
+      // after a wait that gave up: let the copies in flight land
+      const int first = it - S > 0 ? it - S : 0;
+      for (int j = first; !ok && j < it; ++j) drain_wait(&full[j % S], (j / S) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t id0 = idesc_fp4(FMT, 128, C::MMA_N, 0);
+      int it = 0, tc = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++tc) {
+        // 64-column tiles: the second half of a 128-row scale block lies two columns on
+        const uint32_t wcol = C::SMALL ? static_cast<uint32_t>((fp4_tile(p, pre, u, CH).n0 & 64) >> 5) : 0u;
+        const int buf = tc % NB;
+        if (!mbar_wait(&tempty[buf], ((tc / NB) & 1) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem + buf * BN;
+        for (int kb = 0; kb < p.kstages; ++kb, ++it) {
+          const int st = it % S;
+          if (!mbar_wait(&full[st], (it / S) & 1, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sfa = tmem + C::ACC_COLS + (it % C::SFBUF) * C::SF_TMEM;
+          const uint32_t sfb = sfa + C::SF_COLS;
+          const uint8_t* s = sSF + st * C::SF_STAGE;
+          const int nk = min(C::NKB, p.kb - kb * C::NKB);
+          for (int b = 0; b < nk; ++b) {
+            tmem_cp_sf_chunk(sfa + b * 4, s + b * 512);
+#pragma unroll
+            for (int j = 0; j < C::BBLK; ++j)
+              tmem_cp_sf_chunk(sfb + b * C::B_STEP + j * (C::TWO_MMA ? C::SF_COLS : 4),
+                               s + (1 + j) * C::SF_BYTES + b * 512);
+          }
+          const uint64_t ad = smem_desc_kmajor_sw128(sA + st * p.a_bytes);
+          const uint64_t bd = smem_desc_kmajor_sw128(sB + st * C::B_BYTES);
+          const int64_t left = p.K - static_cast<int64_t>(kb) * 256;
+          const int ks = left >= 256 ? 4 : static_cast<int>((left + 63) >> 6);
+#pragma unroll 4
+          for (int k = 0; k < ks; ++k) {
+            // nvfp4: a K slice has a scale block of its own; mxfp4: two share one, ids 0 and 2
+            const int b = FMT == kNv ? k : k >> 1;
+            const uint32_t id = FMT == kNv ? 0u : 2u * (k & 1);
+            const uint32_t idesc = id0 | (id << 4) | (id << 29);
+            const uint32_t sa = (sfa + b * 4) | (id << 30);
+            const uint32_t sb = (sfb + b * C::B_STEP + wcol) | (id << 30);
+            mma_fp4<FMT>(d, ad + 2 * k, bd + 2 * k, idesc, kb > 0 || k > 0, sa, sb);
+            if constexpr (C::TWO_MMA)
+              mma_fp4<FMT>(d + CH, ad + 2 * k, bd + (CH * kStageBytes >> 4) + 2 * k, idesc, kb > 0 || k > 0, sa,
+                           sb + C::SF_COLS);
+          }
+          mma_commit(&empty[st]);
+        }
+        if (ok) mma_commit(&tfull[buf]);
+      }
+      // every MMA issued has completed once `drain` flips
+      mma_commit(drain);
+      drain_wait(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quad = warp & 3;                        // tensor memory lanes 32 quad ..
+    const int r = quad * 32 + lane;                   // this thread's token of the tile
+    const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    const float ga = p.ga ? *p.ga : 1.0f;
+    const float gh = FUSED && p.gh ? *p.gh : 1.0f;
+    constexpr int COLS = CH / (C::EPI_WARPS / 4);     // output columns of a thread
+    const int col0 = ((warp - 2) >> 2) * COLS;
+    int tc = 0;
+    bool ok = true;
+    for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++tc) {
+      const Fp4Tile t = fp4_tile(p, pre, u, CH);
+      const float alpha = p.gb ? ga * p.gb[t.e] : ga;
+      const int buf = tc % NB;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[buf], (tc / NB) & 1, abort_flag, p.status))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t acc = tmem + lane_addr + buf * BN + col0;
+      const int64_t n = t.n0 + col0;
+      if constexpr (!FUSED) {
+        // The thread's columns, rounded to bf16 as they are read, so that the
+        // accumulator goes back to the MMAs before anything is stored.
+        uint32_t o[COLS / 2];
+        if (quad * 32 < t.cnt) {
+#pragma unroll
+          for (int c = 0; c < COLS; c += 32) {
+            uint32_t v[32];
+            tmem_ld_waited<32>(acc + c, v);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              o[(c + i) / 2] = pack_bf16(__uint_as_float(v[i]) * alpha, __uint_as_float(v[i + 1]) * alpha);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[buf]);
+        if (r < t.cnt) {
+          uint16_t* y = p.y + (t.t0 + r) * p.ldy + n;
+          if (p.vec32 && n + COLS <= p.N) {
+#pragma unroll
+            for (int c = 0; c < COLS / 2; c += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + 2 * c),
+                           "r"(o[c]), "r"(o[c + 1]), "r"(o[c + 2]), "r"(o[c + 3]), "r"(o[c + 4]), "r"(o[c + 5]),
+                           "r"(o[c + 6]), "r"(o[c + 7])
+                           : "memory");
+          } else {
+#pragma unroll
+            for (int c = 0; c < COLS / 2; c += 4)
+              if (n + 2 * c < p.N)
+                *reinterpret_cast<uint4*>(y + 2 * c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+          }
+        }
+      } else {
+        // The same gate and up columns of the thread's row; the accumulator
+        // goes back once they are in registers.
+        uint32_t g[COLS], w[COLS];
+        if (quad * 32 < t.cnt) {
+#pragma unroll
+          for (int c = 0; c < COLS; c += 32) {
+            tmem_ld_async<32>(acc + c, g + c);
+            tmem_ld_async<32>(acc + CH + c, w + c);
+          }
+#pragma unroll
+          for (int c = 0; c < COLS; c += 32) {
+            tmem_wait_regs<32>(g + c);
+            tmem_wait_regs<32>(w + c);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[buf]);
+        if (r < t.cnt) {
+          constexpr int G = fp4_group<FMT>();
+          uint32_t code[COLS / 8], sfw = 0;
+#pragma unroll
+          for (int j = 0; j < COLS; j += G) {
+            float y[G], amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+              y[i] = silu_mul_f32(__uint_as_float(g[j + i]) * alpha, __uint_as_float(w[j + i]) * alpha);
+              amax = fmaxf(amax, fabsf(y[i]));
+            }
+            const Fp4Scale s = fp4_scale<FMT>(amax, gh);
+            sfw |= s.byte << (8 * (j / G));
+#pragma unroll
+            for (int i = 0; i < G; i += 8) code[(j + i) / 8] = fp4_codes8<FMT>(y + i, s);
+          }
+          uint4* q = reinterpret_cast<uint4*>(p.hq + (t.t0 + r) * (p.I >> 1) + (n >> 1));
+#pragma unroll
+          for (int c = 0; c < COLS / 8; c += 4)
+            q[c / 4] = make_uint4(code[c], code[c + 1], code[c + 2], code[c + 3]);
+          // tiles begin at a block row of the scales; a thread's scales are aligned 1 to 4 bytes of a word
+          uint8_t* sf = p.hsf + fp4_sf_offset(t.tblk * 128 + r, n / G, fp4_kblocks(FMT, p.I));
+          if constexpr (COLS / G == 4) *reinterpret_cast<uint32_t*>(sf) = sfw;
+          else if constexpr (COLS / G == 2) *reinterpret_cast<uint16_t*>(sf) = static_cast<uint16_t>(sfw);
+          else *sf = static_cast<uint8_t>(sfw);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::TMEM);
+}
+
+// ------------------------------------------------------------------ host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(ptr);
+  });
+  return fn;
+}
+
+// Codes [rows, K / 2] bytes, box = box_rows x 128 bytes, 128-byte swizzle,
+// zero (code 0) outside the matrix.
+bool fp4_tensor_map(const void* ptr, int64_t rows, int64_t K, int box_rows, CUtensorMap* out) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t gdim[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t gstride[1] = {static_cast<cuuint64_t>(K / 2)};
+  const cuuint32_t box[2] = {kStageBytes, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estride[2] = {1, 1};
+  return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), gdim, gstride, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kStaticSmem = 4 * (kMaxExperts + 1) + 12;
+constexpr int kSmemMax = 227 * 1024 - kStaticSmem;
+constexpr int kSmemHalf = 113 * 1024 - kStaticSmem;   // two CTAs in 228 KB, 1 KB of each reserved
+
+template <int FMT, int CH, bool FUSED>
+fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p, cudaStream_t stream) {
+  using C = Fp4Cfg<FMT, CH, FUSED>;
+  CUtensorMap mt, mw;
+  if (!fp4_tensor_map(t, p.M, p.K, p.box, &mt) || !fp4_tensor_map(w, p.E * p.N, p.K, C::BBOX, &mw))
+    return FP8Q_ERR_CUDA;
+  p.tiles_n = static_cast<int>(((FUSED ? p.I : p.N) + CH - 1) / CH);
+  // A tile that is known to have fewer rows keeps less of them; its MMA reads
+  // 128 rows' worth of shared memory from the tile's start all the same, so
+  // the last stage's must stay inside the allocation.
+  p.a_bytes = p.M <= 128 ? static_cast<int>((p.M + p.box - 1) / p.box) * p.box * kStageBytes : 128 * kStageBytes;
+  const int stage = p.a_bytes + C::B_BYTES + C::SF_STAGE;
+  const int slack = 1024 + 256 + 128 * kStageBytes - p.a_bytes;   // alignment, barriers, that reach
+  const int budget = C::SMALL ? kSmemHalf : kSmemMax;
+  p.stages = (budget - slack) / stage;
+  if (p.stages > 12) p.stages = 12;
+  const int smem = p.stages * stage + slack;
+  auto kern = fp4_gemm_kernel<FMT, CH, FUSED>;
+  static std::atomic<int> attr_done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8Q_ERR_CUDA;
+  if (!attr_done[dev].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, budget) != cudaSuccess)
+      return FP8Q_ERR_CUDA;
+    attr_done[dev].store(1, std::memory_order_relaxed);
+  }
+  const int64_t units = tiles_t * p.tiles_n, slots = static_cast<int64_t>(num_sms()) * (C::SMALL ? 2 : 1);
+  const unsigned grid = static_cast<unsigned>(units < slots ? units : slots);
+  return launch_kernel(kern, dim3(grid), dim3(C::THREADS), smem, stream, 1, mt, mw, p);
+}
+
+// Variant and launch.
+template <int FMT, bool FUSED>
+fp8q_status run_fp4(const void* t, const void* w, Fp4Args& p, cudaStream_t stream) {
+  // token tiles: at most this many (an expert's last one may be ragged)
+  const int64_t tt = p.offsets ? p.M / 128 + (p.M < p.E ? p.M : p.E) : (p.M + 127) / 128;
+  const int64_t per = p.offsets ? (p.M + p.E - 1) / p.E : p.M;      // rows of an expert, on average
+  p.box = per > 64 ? 128 : p.M <= 16 ? 16 : 32;
+  const int64_t nw = FUSED ? p.I : p.N, sms = num_sms();
+  if constexpr (FUSED) {
+    if (tt * (nw / 128) < sms) return launch_fp4<FMT, 64, true>(t, w, tt, p, stream);
+    return launch_fp4<FMT, 128, true>(t, w, tt, p, stream);
+  } else {
+    if (per <= 64 || tt * ((nw + 127) / 128) < sms) return launch_fp4<FMT, 64, false>(t, w, tt, p, stream);
+    if (tt * ((nw + 255) / 256) < sms) return launch_fp4<FMT, 128, false>(t, w, tt, p, stream);
+    return launch_fp4<FMT, 256, false>(t, w, tt, p, stream);
+  }
+}
+
+// Sizes, alignment and the argument block shared by the entry points.  Row
+// coordinates and tile counts are 32 bits.
+constexpr int64_t kMax32 = int64_t{1} << 31;
+
+fp8q_status check_mm(const void* a_q, const void* b_q, const uint8_t* a_sf, const uint8_t* b_sf, int format,
+                     const float* ga, const float* gb, int64_t E, int64_t M, int64_t N, int64_t K, Fp4Args* p) {
+  if (format != FP8Q_FP4_NV && format != FP8Q_FP4_MX) return FP8Q_ERR_INVALID_ARG;
+  if (M < 0 || N <= 0 || K <= 0 || N % 16 != 0 || K % 32 != 0 || E <= 0) return FP8Q_ERR_INVALID_ARG;
+  if (E > kMaxExperts) return FP8Q_ERR_UNSUPPORTED;
+  if (format == FP8Q_FP4_MX && (ga || gb)) return FP8Q_ERR_INVALID_ARG;
+  if (M >= kMax32 || N >= kMax32 || K >= kMax32 || E * N >= kMax32 || (M / 128 + E) * ((N + 63) / 64) >= kMax32)
+    return FP8Q_ERR_INVALID_ARG;
+  if (M == 0) return FP8Q_OK;
+  if (!a_q || !b_q || !a_sf || !b_sf) return FP8Q_ERR_INVALID_ARG;
+  if (!aligned(a_q, 16) || !aligned(b_q, 16) || !aligned(a_sf, 16) || !aligned(b_sf, 16) || !aligned(ga, 4) ||
+      !aligned(gb, 4))
+    return FP8Q_ERR_INVALID_ARG;
+  p->M = M;
+  p->N = N;
+  p->K = K;
+  p->sft = a_sf;
+  p->sfw = b_sf;
+  p->kb = static_cast<int>(fp4_kblocks(format, K));
+  p->kstages = static_cast<int>((K + 255) / 256);
+  p->wblocks = (N + 127) / 128;
+  p->ga = ga;
+  p->gb = gb;
+  p->E = static_cast<int>(E);
+  p->status = device_status_ptr();
+  return FP8Q_OK;
+}
+
+fp8q_status check_y(void* y, int64_t ldy, int64_t M, int64_t N, Fp4Args* p) {
+  if (ldy < N || ldy % 8 != 0 || (M > 0 && (!y || !aligned(y, 16)))) return FP8Q_ERR_INVALID_ARG;
+  p->y = static_cast<uint16_t*>(y);
+  p->ldy = ldy;
+  p->vec32 = aligned(y, 32) && ldy % 16 == 0;
+  return FP8Q_OK;
+}
+
+fp8q_status check_groups(const int* offsets, const int* sf_offsets, int64_t M, Fp4Args* p) {
+  if (M > 0 && (!offsets || !sf_offsets || !aligned(offsets, 4) || !aligned(sf_offsets, 4))) return FP8Q_ERR_INVALID_ARG;
+  p->offsets = offsets;
+  p->sf_offsets = sf_offsets;
+  return FP8Q_OK;
+}
+
+}  // namespace
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" fp8q_status fp8q_scaled_mm_fp4(const void* a_q, const void* b_q, const uint8_t* a_sf, const uint8_t* b_sf,
+                                          int format, const float* a_gscale, const float* b_gscale, int64_t M,
+                                          int64_t N, int64_t K, void* y, int64_t ldy, void* stream) {
+  Fp4Args p{};
+  fp8q_status st = check_mm(a_q, b_q, a_sf, b_sf, format, a_gscale, b_gscale, 1, M, N, K, &p);
+  if (st == FP8Q_OK) st = check_y(y, ldy, M, N, &p);
+  if (st != FP8Q_OK || M == 0) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return format == FP8Q_FP4_NV ? run_fp4<kNv, false>(a_q, b_q, p, s) : run_fp4<kMx, false>(a_q, b_q, p, s);
+}
+
+extern "C" fp8q_status fp8q_grouped_mm_fp4(const void* a_q, const void* b_q, const uint8_t* a_sf, const uint8_t* b_sf,
+                                           int format, const float* a_gscale, const float* b_gscale, const int* offsets,
+                                           const int* sf_offsets, int64_t E, int64_t M, int64_t N, int64_t K, void* y,
+                                           int64_t ldy, void* stream) {
+  Fp4Args p{};
+  fp8q_status st = check_mm(a_q, b_q, a_sf, b_sf, format, a_gscale, b_gscale, E, M, N, K, &p);
+  if (st == FP8Q_OK) st = check_y(y, ldy, M, N, &p);
+  if (st == FP8Q_OK) st = check_groups(offsets, sf_offsets, M, &p);
+  if (st != FP8Q_OK || M == 0) return st;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return format == FP8Q_FP4_NV ? run_fp4<kNv, false>(a_q, b_q, p, s) : run_fp4<kMx, false>(a_q, b_q, p, s);
+}
+
+extern "C" fp8q_status fp8q_grouped_mm_fp4_silu_quant(const void* a_q, const void* b_q, const uint8_t* a_sf,
+                                                      const uint8_t* b_sf, int format, const float* a_gscale,
+                                                      const float* b_gscale, const int* offsets, const int* sf_offsets,
+                                                      int64_t E, int64_t M, int64_t I, int64_t K, const float* gscale,
+                                                      void* q, uint8_t* sf, void* stream) {
+  if (I <= 0 || I >= kMax32) return FP8Q_ERR_INVALID_ARG;
+  Fp4Args p{};
+  fp8q_status st = check_mm(a_q, b_q, a_sf, b_sf, format, a_gscale, b_gscale, E, M, 2 * I, K, &p);
+  if (st == FP8Q_OK && I % 128 != 0) st = FP8Q_ERR_UNSUPPORTED;
+  if (st == FP8Q_OK) st = check_groups(offsets, sf_offsets, M, &p);
+  if (st != FP8Q_OK) return st;
+  if (format == FP8Q_FP4_MX && gscale) return FP8Q_ERR_INVALID_ARG;
+  if (M == 0) return FP8Q_OK;
+  if (!q || !sf || !aligned(q, 16) || !aligned(sf, 16) || !aligned(gscale, 4)) return FP8Q_ERR_INVALID_ARG;
+  p.I = I;
+  p.hq = static_cast<uint8_t*>(q);
+  p.hsf = sf;
+  p.gh = gscale;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return format == FP8Q_FP4_NV ? run_fp4<kNv, true>(a_q, b_q, p, s) : run_fp4<kMx, true>(a_q, b_q, p, s);
+}

@@ -1,0 +1,408 @@
+// fp8q_fp4_quant.cu -- 4-bit microscaled quantization (nvfp4, mxfp4) of bf16
+// rows, plain or fused with its producer (RMSNorm, SiLU*mul), its scatter into
+// the experts' rows, and the way back to values.
+//
+// HBM-bound: a row's values are read once (2 bytes each, SiLU*mul 4) and
+// leave as half a byte each plus a scale byte per group.  The unit of work is
+// an item of 16 neighbouring values of a row, one 32-byte load: an nvfp4
+// group, or half an mxfp4 one (the two halves sit in neighbouring lanes and
+// exchange their amax by one shuffle).  y is the exact bf16 value of its
+// definition, as in the FP8 quant kernels (the same brackets, the same rare
+// fp64 recomputation), so codes and scales equal the definition bit for bit.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fp8q_common.cuh"
+#include "fp8q_fp4_math.cuh"
+#include "fp8q_quant_math.cuh"
+
+namespace fp8q {
+namespace {
+
+enum { OP_PLAIN = 0, OP_SILU = 1 };
+
+struct Fp4QuantParams {
+  const uint16_t* x;         // bf16 [M, K] ([M, 2K] = [gate | up] for SiLU), leading dimension ldx
+  int64_t M, K, ldx;
+  const uint16_t* w;         // RMSNorm weight [K]
+  float eps;
+  const float* g;            // tensor scale or null
+  uint8_t* q;                // codes, ldq bytes a row
+  int64_t ldq;
+  uint8_t* sf;               // scale blocks, kb to a block row
+  int64_t kb;
+  const int* pos;            // scatter: [M, topk] destination rows (negative: none) and scale rows
+  const int* sf_row;
+  int topk;
+};
+
+// Items are 16 values: two 16-byte chunks of 8.
+struct Item {
+  uint4 a, b;
+};
+
+__device__ __forceinline__ Item ld_item(const uint16_t* p, bool wide) {
+  Item v;
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.a.x), "=r"(v.a.y), "=r"(v.a.z), "=r"(v.a.w), "=r"(v.b.x), "=r"(v.b.y), "=r"(v.b.z),
+                   "=r"(v.b.w)
+                 : "l"(p));
+  } else {
+    v.a = __ldg(reinterpret_cast<const uint4*>(p));
+    v.b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint4 silu_chunk(const uint4& g, const uint4& u) {
+  uint32_t d = 0;
+  bool bad = false;
+  uint4 y;
+  y.x = silu_pair(g.x, u.x, d, bad);
+  y.y = silu_pair(g.y, u.y, d, bad);
+  y.z = silu_pair(g.z, u.z, d, bad);
+  y.w = silu_pair(g.w, u.w, d, bad);
+  return (d | bad) ? silu_chunk_fix(g, u, y) : y;
+}
+
+__device__ __forceinline__ void chunk_to_f32(const uint4& c, float* f) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// Codes and scale of one item, y already bf16.  mxfp4: every lane of a pair
+// must call it (shuffle); a lane without an item passes zeros.
+template <int FMT>
+__device__ __forceinline__ uint2 item_codes(const Item& y, float g, uint32_t* byte) {
+  float amax = absmax2_to_f32(chunk_absmax2(y.b, chunk_absmax2(y.a, 0u)));
+  if constexpr (FMT == kMx) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  const Fp4Scale s = fp4_scale<FMT>(amax, g);
+  float f[8];
+  uint2 c;
+  chunk_to_f32(y.a, f);
+  c.x = fp4_codes8<FMT>(f, s);
+  chunk_to_f32(y.b, f);
+  c.y = fp4_codes8<FMT>(f, s);
+  *byte = s.byte;
+  return c;
+}
+
+// Store item `it` (of K / 16) of a row: its codes at row `row`, its group's
+// scale at scale row `srow`; the last item of a row also zeroes the bytes of
+// the groups that fill its last scale block.
+template <int FMT>
+__device__ __forceinline__ void store_item(const Fp4QuantParams& p, int64_t row, int64_t srow, int it, int items,
+                                           const uint2& c, uint32_t byte) {
+  *reinterpret_cast<uint2*>(p.q + row * p.ldq + 8 * it) = c;
+  const int group = FMT == kNv ? it : it >> 1;
+  if (FMT == kNv || (it & 1) == 0) p.sf[fp4_sf_offset(srow, group, p.kb)] = static_cast<uint8_t>(byte);
+  if (it == items - 1)
+    for (int j = group + 1; j & 3; ++j) p.sf[fp4_sf_offset(srow, j, p.kb)] = 0;
+}
+
+template <int FMT>
+__device__ __forceinline__ void emit_item(const Fp4QuantParams& p, int64_t row, int it, int items, const uint2& c,
+                                          uint32_t byte) {
+  if (p.pos == nullptr) {
+    store_item<FMT>(p, row, row, it, items, c, byte);
+  } else {
+    for (int j = 0; j < p.topk; ++j) {
+      const int dst = __ldg(p.pos + row * p.topk + j);
+      if (dst >= 0) store_item<FMT>(p, dst, __ldg(p.sf_row + row * p.topk + j), it, items, c, byte);
+    }
+  }
+}
+
+// Plain and SiLU*mul: independent items, one a thread and step.
+constexpr int kItemThreads = 256;
+
+template <int FMT, int OP>
+__global__ void __launch_bounds__(kItemThreads) fp4_items_kernel(const Fp4QuantParams p, int wide) {
+  const int items = static_cast<int>(p.K >> 4);
+  const int64_t total = p.M * items;
+  griddep_wait();
+  griddep_launch_dependents();
+  const float g = p.g ? *p.g : 1.0f;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kItemThreads;
+  // whole warps stay in the loop: total is even, so pairs of lanes live and end together
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kItemThreads + (threadIdx.x & ~31); i0 < total; i0 += stride) {
+    const int64_t i = i0 + (threadIdx.x & 31);
+    const bool live = i < total;
+    const int64_t row = live ? (total <= 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(items)) : i / items) : 0;
+    const int it = live ? static_cast<int>(i - row * items) : 0;
+    Item y = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    if (live) {
+      const uint16_t* x = p.x + row * p.ldx + 16 * it;
+      y = ld_item(x, wide);
+      if constexpr (OP == OP_SILU) {
+        const Item u = ld_item(x + p.K, wide);
+        y.a = silu_chunk(y.a, u.a);
+        y.b = silu_chunk(y.b, u.b);
+      }
+    }
+    uint32_t byte;
+    const uint2 c = item_codes<FMT>(y, g, &byte);
+    if (live) emit_item<FMT>(p, row, it, items, c, byte);
+  }
+}
+
+// RMSNorm: one CTA a row.  y = bf16(bf16(x r) w), r = 1/sqrt(mean(x^2) + eps);
+// the sum of squares in fp64.  IT items a thread stay in registers between the
+// two passes; IT = 0 (rows of any length) reads them again.
+template <int FMT, int IT>
+__global__ void __launch_bounds__(512) fp4_rms_kernel(const Fp4QuantParams p, int wide) {
+  __shared__ double red[32];
+  const int items = static_cast<int>(p.K >> 4);
+  const int T = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Item zero = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  griddep_wait();
+  griddep_launch_dependents();
+  const float g = p.g ? *p.g : 1.0f;
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
+    const uint16_t* x = p.x + row * p.ldx;
+    Item v[IT ? IT : 1];
+    double ss = 0.0;
+    auto add = [&](const Item& a) {
+      float f[16];
+      chunk_to_f32(a.a, f);
+      chunk_to_f32(a.b, f + 8);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = __fma_rn(static_cast<double>(f[i]), static_cast<double>(f[i]), ss);
+    };
+    if constexpr (IT > 0) {
+#pragma unroll
+      for (int k = 0; k < IT; ++k) v[k] = tid + k * T < items ? ld_item(x + 16 * (tid + k * T), wide) : zero;
+#pragma unroll
+      for (int k = 0; k < IT; ++k) add(v[k]);
+    } else {
+      for (int it = tid; it < items; it += T) add(ld_item(x + 16 * it, wide));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    __syncthreads();                       // red is free again
+    if (lane == 0) red[warp] = ss;
+    __syncthreads();
+    ss = 0.0;
+    for (int i = 0; i < (T >> 5); ++i) ss += red[i];
+    float r_lo, r_hi;
+    rms_bracket(ss / static_cast<double>(p.K) + static_cast<double>(p.eps), r_lo, r_hi);
+    const uint64_t rlo2 = dup2(r_lo), rhi2 = dup2(r_hi);
+    auto norm = [&](const uint4& xv, const uint4& wv) {
+      uint32_t d = 0;
+      uint4 y;
+      y.x = bf2_mul(rms_n_pair(xv.x, rlo2, rhi2, d), wv.x);
+      y.y = bf2_mul(rms_n_pair(xv.y, rlo2, rhi2, d), wv.y);
+      y.z = bf2_mul(rms_n_pair(xv.z, rlo2, rhi2, d), wv.z);
+      y.w = bf2_mul(rms_n_pair(xv.w, rlo2, rhi2, d), wv.w);
+      return d ? rms_chunk_fix(xv, wv, y, rlo2, rhi2, ss, p.K, p.eps) : y;
+    };
+    const int steps = IT ? IT : (items + T - 1) / T;
+#pragma unroll
+    for (int k = 0; k < steps; ++k) {
+      const int it = tid + k * T;
+      const bool live = it < items;
+      Item y = zero;
+      if (live) {
+        const Item a = IT ? v[IT ? k : 0] : ld_item(x + 16 * it, wide);
+        const uint4* wp = reinterpret_cast<const uint4*>(p.w) + 2 * it;
+        y.a = norm(a.a, __ldg(wp));
+        y.b = norm(a.b, __ldg(wp + 1));
+      }
+      uint32_t byte;
+      const uint2 c = item_codes<FMT>(y, g, &byte);
+      if (live) store_item<FMT>(p, row, row, it, items, c, byte);
+    }
+  }
+}
+
+// Values: bf16_rn(fl32(fl32(code sf) g)), an item a thread and step.
+template <int FMT>
+__global__ void __launch_bounds__(kItemThreads)
+    fp4_dequant_kernel(const uint8_t* q, int64_t ldq, const uint8_t* sf, int64_t kb, const float* gp, int64_t M,
+                       int64_t K, uint16_t* y, int64_t ldy) {
+  const int items = static_cast<int>(K >> 4);
+  const int64_t total = M * items;
+  griddep_wait();
+  griddep_launch_dependents();
+  const float g = gp ? *gp : 1.0f;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kItemThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kItemThreads) {
+    const int64_t row = total <= 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(items)) : i / items;
+    const int it = static_cast<int>(i - row * items);
+    const uint2 c = *reinterpret_cast<const uint2*>(q + row * ldq + 8 * it);
+    const uint32_t b = sf[fp4_sf_offset(row, FMT == kNv ? it : it >> 1, kb)];
+    float s;
+    if constexpr (FMT == kNv) {
+      s = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3)));
+    } else {
+      s = b ? __uint_as_float(b << 23) : __uint_as_float(0x00400000u);   // 255 -> infinity
+      if (b == 255u) s = __uint_as_float(0x7FFFFFFFu);                   // E8M0 NaN
+    }
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      uint32_t h2;
+      const uint16_t byte = static_cast<uint16_t>(((k < 4 ? c.x : c.y) >> (8 * (k & 3))) & 0xFFu);
+      asm("{\n\t.reg .b8 lo, hi;\n\t"
+          "mov.b16 {lo, hi}, %1;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %0, lo;\n\t}"
+          : "=r"(h2)
+          : "h"(byte));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+      const __nv_bfloat162 v = __floats2bfloat162_rn(__fmul_rn(__fmul_rn(f.x, s), g), __fmul_rn(__fmul_rn(f.y, s), g));
+      o[k] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    uint4* d = reinterpret_cast<uint4*>(y + row * ldy + 16 * it);
+    d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+// Blocks of the item kernels: enough that each thread has about one item, but
+// no more than 16 resident blocks' worth a pass (they stride).
+unsigned item_blocks(int64_t total) {
+  int64_t b = (total + kItemThreads - 1) / kItemThreads;
+  const int64_t cap = static_cast<int64_t>(num_sms()) * 32;
+  return static_cast<unsigned>(b < cap ? b : cap);
+}
+
+template <int FMT, int OP>
+fp8q_status launch_items(const Fp4QuantParams& p, cudaStream_t stream) {
+  const int wide = aligned(p.x, 32) && p.ldx % 16 == 0;
+  return launch_kernel(fp4_items_kernel<FMT, OP>, dim3(item_blocks(p.M * (p.K >> 4))), dim3(kItemThreads), 0, stream,
+                       1, p, wide);
+}
+
+template <int FMT>
+fp8q_status launch_rms(const Fp4QuantParams& p, cudaStream_t stream) {
+  const int wide = aligned(p.x, 32) && p.ldx % 16 == 0;
+  const int64_t items = p.K >> 4;
+  // threads: whole warps, at most 512; items a thread as few as that allows
+  const int it = items <= 512 ? 1 : items <= 1024 ? 2 : items <= 2048 ? 4 : 0;
+  const int64_t need = it ? (items + it - 1) / it : 512;
+  const int T = static_cast<int>((need + 31) / 32 * 32);
+  const int64_t cap = static_cast<int64_t>(num_sms()) * (2048 / T) * 4;
+  const dim3 grid(static_cast<unsigned>(p.M < cap ? p.M : cap)), block(T);
+  switch (it) {
+    case 1: return launch_kernel(fp4_rms_kernel<FMT, 1>, grid, block, 0, stream, 1, p, wide);
+    case 2: return launch_kernel(fp4_rms_kernel<FMT, 2>, grid, block, 0, stream, 1, p, wide);
+    case 4: return launch_kernel(fp4_rms_kernel<FMT, 4>, grid, block, 0, stream, 1, p, wide);
+    default: return launch_kernel(fp4_rms_kernel<FMT, 0>, grid, block, 0, stream, 1, p, wide);
+  }
+}
+
+// Sizes and pointers shared by the quant entry points; *go is set when there
+// is work to launch.
+fp8q_status check_quant(const void* x, int64_t M, int64_t K, int64_t width, int64_t ldx, int format, const float* g,
+                        const void* q, int64_t ldq, const void* sf, bool* go) {
+  *go = false;
+  if (format != FP8Q_FP4_NV && format != FP8Q_FP4_MX) return FP8Q_ERR_INVALID_ARG;
+  if (M < 0 || K <= 0 || K % 32 != 0 || K > (int64_t{1} << 30) || M >= (int64_t{1} << 31)) return FP8Q_ERR_INVALID_ARG;
+  if (ldx < width || ldx % 8 != 0 || ldq < K / 2 || ldq % 8 != 0) return FP8Q_ERR_INVALID_ARG;
+  if (format == FP8Q_FP4_MX && g) return FP8Q_ERR_INVALID_ARG;
+  if (M == 0) return FP8Q_OK;
+  if (!x || !q || !sf) return FP8Q_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16) || !aligned(g, 4)) return FP8Q_ERR_INVALID_ARG;
+  *go = true;
+  return FP8Q_OK;
+}
+
+Fp4QuantParams quant_params(const void* x, int64_t M, int64_t K, int64_t ldx, int format, const float* g, void* q,
+                            int64_t ldq, uint8_t* sf) {
+  Fp4QuantParams p{};
+  p.x = static_cast<const uint16_t*>(x);
+  p.M = M;
+  p.K = K;
+  p.ldx = ldx;
+  p.g = g;
+  p.q = static_cast<uint8_t*>(q);
+  p.ldq = ldq;
+  p.sf = sf;
+  p.kb = fp4_kblocks(format, K);
+  return p;
+}
+
+}  // namespace
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" size_t fp8q_fp4_sf_bytes(int64_t rows, int64_t K, int format) {
+  if (rows <= 0 || K <= 0 || (format != FP8Q_FP4_NV && format != FP8Q_FP4_MX)) return 0;
+  return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>(fp4_kblocks(format, K)) * 512;
+}
+
+extern "C" fp8q_status fp8q_fp4_quant(const void* x, int64_t M, int64_t K, int64_t ldx, int format,
+                                      const float* gscale, void* q, int64_t ldq, uint8_t* sf, void* stream) {
+  bool go;
+  const fp8q_status st = check_quant(x, M, K, K, ldx, format, gscale, q, ldq, sf, &go);
+  if (!go) return st;
+  const Fp4QuantParams p = quant_params(x, M, K, ldx, format, gscale, q, ldq, sf);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return format == FP8Q_FP4_NV ? launch_items<kNv, OP_PLAIN>(p, s) : launch_items<kMx, OP_PLAIN>(p, s);
+}
+
+extern "C" fp8q_status fp8q_silu_mul_fp4_quant(const void* x, int64_t M, int64_t I, int64_t ldx, int format,
+                                               const float* gscale, void* q, int64_t ldq, uint8_t* sf, void* stream) {
+  bool go;
+  const fp8q_status st = check_quant(x, M, I, 2 * I, ldx, format, gscale, q, ldq, sf, &go);
+  if (!go) return st;
+  const Fp4QuantParams p = quant_params(x, M, I, ldx, format, gscale, q, ldq, sf);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return format == FP8Q_FP4_NV ? launch_items<kNv, OP_SILU>(p, s) : launch_items<kMx, OP_SILU>(p, s);
+}
+
+extern "C" fp8q_status fp8q_rmsnorm_fp4_quant(const void* x, const void* w, float eps, int64_t M, int64_t H,
+                                              int64_t ldx, int format, const float* gscale, void* q, int64_t ldq,
+                                              uint8_t* sf, void* stream) {
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return FP8Q_ERR_INVALID_ARG;
+  bool go;
+  const fp8q_status st = check_quant(x, M, H, H, ldx, format, gscale, q, ldq, sf, &go);
+  if (!go) return st;
+  if (!w || !aligned(w, 16)) return FP8Q_ERR_INVALID_ARG;
+  Fp4QuantParams p = quant_params(x, M, H, ldx, format, gscale, q, ldq, sf);
+  p.w = static_cast<const uint16_t*>(w);
+  p.eps = eps;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return format == FP8Q_FP4_NV ? launch_rms<kNv>(p, s) : launch_rms<kMx>(p, s);
+}
+
+extern "C" fp8q_status fp8q_moe_fp4_quant(const void* x, int64_t T, int64_t K, int64_t ldx, int topk, const int* pos,
+                                          const int* sf_row, int format, const float* gscale, void* q, int64_t ldq,
+                                          uint8_t* sf, void* stream) {
+  if (topk <= 0) return FP8Q_ERR_INVALID_ARG;
+  bool go;
+  const fp8q_status st = check_quant(x, T, K, K, ldx, format, gscale, q, ldq, sf, &go);
+  if (!go) return st;
+  if (!pos || !sf_row || !aligned(pos, 4) || !aligned(sf_row, 4)) return FP8Q_ERR_INVALID_ARG;
+  Fp4QuantParams p = quant_params(x, T, K, ldx, format, gscale, q, ldq, sf);
+  p.pos = pos;
+  p.sf_row = sf_row;
+  p.topk = topk;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return format == FP8Q_FP4_NV ? launch_items<kNv, OP_PLAIN>(p, s) : launch_items<kMx, OP_PLAIN>(p, s);
+}
+
+extern "C" fp8q_status fp8q_fp4_dequant(const void* q, int64_t ldq, const uint8_t* sf, int format,
+                                        const float* gscale, int64_t M, int64_t K, void* y, int64_t ldy,
+                                        void* stream) {
+  if (format != FP8Q_FP4_NV && format != FP8Q_FP4_MX) return FP8Q_ERR_INVALID_ARG;
+  if (M < 0 || K <= 0 || K % 32 != 0 || K > (int64_t{1} << 30) || M >= (int64_t{1} << 31)) return FP8Q_ERR_INVALID_ARG;
+  if (ldq < K / 2 || ldq % 8 != 0 || ldy < K || ldy % 8 != 0) return FP8Q_ERR_INVALID_ARG;
+  if (format == FP8Q_FP4_MX && gscale) return FP8Q_ERR_INVALID_ARG;
+  if (M == 0) return FP8Q_OK;
+  if (!q || !sf || !y || !aligned(q, 16) || !aligned(sf, 16) || !aligned(y, 16) || !aligned(gscale, 4))
+    return FP8Q_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto kern = format == FP8Q_FP4_NV ? fp4_dequant_kernel<kNv> : fp4_dequant_kernel<kMx>;
+  return launch_kernel(kern, dim3(item_blocks(M * (K >> 4))), dim3(kItemThreads), 0, s, 1,
+                       static_cast<const uint8_t*>(q), ldq, sf, fp4_kblocks(format, K), gscale, M, K,
+                       static_cast<uint16_t*>(y), ldy);
+}

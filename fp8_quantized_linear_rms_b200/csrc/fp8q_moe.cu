@@ -1,0 +1,527 @@
+// fp8q_moe.cu -- routing to experts and what surrounds their products: the
+// router (scores, selection, weights), the plan that orders (token, expert)
+// pairs by expert, the weighted sum of the experts' rows, and the whole pass.
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "fp8q_common.cuh"
+#include "fp8q_fp4_math.cuh"
+
+namespace fp8q {
+namespace {
+
+constexpr int kMaxExperts = 512;
+constexpr int kMaxTopk = 32;
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+// ------------------------------------------------------------------- router
+struct RouteParams {
+  const void* logits;        // fp32 or bf16 [T, E], leading dimension ld
+  int64_t T, ld;
+  int E, bf16, sigmoid;
+  const float* bias;         // [E] or null
+  int groups, topg, topk, renorm;
+  float scale;
+  float* w;                  // [T, topk]
+  int* ids;                  // [T, topk]
+};
+
+// A NaN counts as -inf (masked); -0 as 0, so that keys are equal where values are.
+__device__ __forceinline__ float route_logit(const RouteParams& p, int64_t t, int e) {
+  const float v = p.bf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.logits) + t * p.ld + e)) << 16)
+                         : __ldg(static_cast<const float*>(p.logits) + t * p.ld + e);
+  return v != v ? -INFINITY : v + 0.0f;
+}
+
+// Order-preserving integers of floating numbers; 0 is below all of them.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t order_key(double v) {
+  const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
+  return (u >> 63) ? ~u : u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ float key_float(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+__device__ __forceinline__ double key_double(uint64_t k) {
+  return __longlong_as_double(static_cast<long long>((k >> 63) ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
+}
+
+// Maximum over the warp.
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kAll, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+  const uint32_t hi = static_cast<uint32_t>(v >> 32);
+  const uint32_t mh = __reduce_max_sync(kAll, hi);
+  const uint32_t ml = __reduce_max_sync(kAll, hi == mh ? static_cast<uint32_t>(v) : 0u);
+  return (static_cast<uint64_t>(mh) << 32) | ml;
+}
+
+// One warp a token; lane holds experts lane, lane + 32, ... (V of them).  Key:
+// the 32-bit order of the logit where the selection has no bias (both scores
+// grow with the logit, so this is the exact order), else the 64-bit order of
+// score + bias in fp64: two biased scores that differ in exact arithmetic
+// differ there too, but for accidents below 2^-50.  Equal keys go to the
+// lowest expert.
+template <int V, typename Key>
+__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  griddep_wait();
+  griddep_launch_dependents();
+  if (t >= p.T) return;
+
+  constexpr bool BIASED = sizeof(Key) == 8;
+  float l[V];
+  Key key[V];
+  uint32_t top = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = v * 32 + lane;
+    l[v] = e < p.E ? route_logit(p, t, e) : -INFINITY;
+    if (e < p.E) top = max(top, order_key(l[v]));
+  }
+  // softmax: the largest logit and the sum of exponentials (terms equal to the
+  // maximum count 1, infinite ones too); no sum where every logit is masked
+  float m = 0.0f, z = 1.0f;
+  double zd = 1.0;
+  if (!p.sigmoid) {
+    m = key_float(warp_max(top));
+    z = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (l[v] > -INFINITY) z += l[v] == m ? 1.0f : expf(l[v] - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
+    if constexpr (BIASED) {
+      zd = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (l[v] > -INFINITY) zd += l[v] == m ? 1.0 : exp(static_cast<double>(l[v]) - static_cast<double>(m));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(kAll, zd, o);
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = v * 32 + lane;
+    key[v] = 0;
+    if (e < p.E) {
+      if constexpr (BIASED) {
+        double c = -INFINITY;
+        if (l[v] > -INFINITY) {
+          const double ld = l[v];
+          const double s = p.sigmoid ? 1.0 / (1.0 + exp(-ld))
+                                     : (l[v] == m ? 1.0 : exp(ld - static_cast<double>(m))) / zd;
+          c = s + static_cast<double>(__ldg(p.bias + e)) + 0.0;
+        }
+        key[v] = order_key(c);
+      } else {
+        key[v] = order_key(l[v]);
+      }
+    }
+  }
+
+  // groups of neighbouring experts: a group's score is its largest key, or
+  // with a bias the sum of its two largest; experts outside the best topg
+  // groups get key 0
+  if (p.topg < p.groups) {
+    const int size = p.E / p.groups;
+    Key mine = 0;                       // lane g: group g's score
+    for (int g = 0; g < p.groups; ++g) {
+      Key a = 0, b = 0;                 // the lane's two largest of the group
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = v * 32 + lane;
+        if (e >= g * size && e < (g + 1) * size) {
+          if (key[v] > a) { b = a; a = key[v]; }
+          else if (key[v] > b) b = key[v];
+        }
+      }
+      Key s = warp_max(a);
+      if constexpr (BIASED) {
+        if (size > 1) {
+          const int owner = __ffs(__ballot_sync(kAll, a == s)) - 1;
+          const Key second = warp_max(lane == owner ? b : a);
+          s = order_key(key_double(s) + key_double(second) + 0.0);
+        }
+      }
+      if (lane == g) mine = s;
+    }
+    uint32_t keep = 0;
+    for (int j = 0; j < p.topg; ++j) {
+      const Key s = warp_max(mine);
+      const int g = __ffs(__ballot_sync(kAll, mine == s && lane < p.groups && !((keep >> lane) & 1u))) - 1;
+      keep |= 1u << g;
+      if (lane == g) mine = 0;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = v * 32 + lane;
+      if (e < p.E && !((keep >> (e / size)) & 1u)) key[v] = 0;
+    }
+  }
+
+  int id = 0;                           // lane j: the j-th expert
+  for (int j = 0; j < p.topk; ++j) {
+    Key a = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) a = key[v] > a ? key[v] : a;
+    const Key best = warp_max(a);
+    uint32_t e = 0xFFFFFFFFu;           // the lane's first expert with it
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v)
+      if (key[v] == best) e = v * 32 + lane;
+    e = __reduce_min_sync(kAll, e);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (e == static_cast<uint32_t>(v * 32 + lane)) key[v] = 0;
+    if (lane == j) id = static_cast<int>(e);
+  }
+
+  float s = 0.0f;
+  if (lane < p.topk) {
+    const float x = route_logit(p, t, id);
+    if (p.sigmoid) s = 1.0f / (1.0f + expf(-x));
+    else if (x > -INFINITY) s = (x == m ? 1.0f : expf(x - m)) / z;
+  }
+  if (p.renorm) {
+    float sum = s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    s = sum > 0.0f ? s / sum : 0.0f;    // no selected expert has a score: no weight
+  }
+  if (lane < p.topk) {
+    p.w[t * p.topk + lane] = s * p.scale;
+    p.ids[t * p.topk + lane] = id;
+  }
+}
+
+// --------------------------------------------------------------------- plan
+// A stable counting sort of n (token, slot) entries by expert, in entry order
+// within an expert, without atomics on results: every count and rank comes
+// from a fixed order.  A block takes up to kPlanBlock entries, a warp a
+// contiguous part of them; __match_any_sync gives the ranks inside 32 entries.
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanBlock = 4096;
+
+struct PlanParams {
+  const int* ids;
+  int n, E, blocks;
+  int* offsets;      // [E + 1]
+  int* sf_offsets;   // [E + 1]
+  int* pos;          // [n]
+  int* sf_row;       // [n]
+  int* hist;         // [blocks, E] counts of the blocks (blocks > 1)
+};
+
+// Counts of the warp's entries [i0, i1) into cnt[E] (shared, the warp's own).
+__device__ __forceinline__ void warp_count(const PlanParams& p, int i0, int i1, int* cnt, int lane) {
+  for (int i = i0; i < i1; i += 32) {
+    const int e = i + lane < i1 ? __ldg(p.ids + i + lane) : -1;
+    const bool in = e >= 0 && e < p.E;
+    const unsigned same = __match_any_sync(kAll, in ? e : -1);
+    if (in && lane == __ffs(same) - 1) cnt[e] += __popc(same);
+    __syncwarp();
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanParams p) {
+  extern __shared__ int cnt[];                          // [warps][E]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kPlanWarps * p.E; i += kPlanThreads) cnt[i] = 0;
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  const int part = kPlanBlock / kPlanWarps;
+  const int i0 = blockIdx.x * kPlanBlock + warp * part;
+  warp_count(p, i0, min(p.n, i0 + part), cnt + warp * p.E, lane);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
+    int s = 0;
+    for (int w = 0; w < kPlanWarps; ++w) s += cnt[w * p.E + e];
+    p.hist[blockIdx.x * p.E + e] = s;
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanParams p) {
+  extern __shared__ int cnt[];                          // [warps][E]: counts, then first ranks of the warps
+  __shared__ int first[kMaxExperts + 1], sf_first[kMaxExperts + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < kPlanWarps * p.E; i += kPlanThreads) cnt[i] = 0;
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  // one block: parts of whole 32-entry steps spread over the warps
+  const int per = p.blocks > 1 ? kPlanBlock : (p.n + kPlanWarps * 32 - 1) / (kPlanWarps * 32) * (kPlanWarps * 32);
+  const int part = per / kPlanWarps;
+  const int i0 = min(p.n, static_cast<int>(blockIdx.x) * per + warp * part);
+  const int i1 = min(p.n, i0 + part);
+  warp_count(p, i0, i1, cnt + warp * p.E, lane);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
+    // the expert's entries in the blocks before this one, in all, and before each warp
+    int before = 0, total = 0;
+    if (p.blocks > 1) {
+      for (int b = 0; b < p.blocks; ++b) {
+        const int c = p.hist[b * p.E + e];
+        if (b < static_cast<int>(blockIdx.x)) before += c;
+        total += c;
+      }
+    }
+    int run = before;
+    for (int w = 0; w < kPlanWarps; ++w) {
+      const int c = cnt[w * p.E + e];
+      cnt[w * p.E + e] = run;
+      run += c;
+    }
+    first[e + 1] = p.blocks > 1 ? total : run;
+  }
+  __syncthreads();
+  if (warp == 0) {                                      // sums over experts
+    int rows = 0, blocks = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int c = e0 + lane < p.E ? first[e0 + lane + 1] : 0;
+      int v = c, b = (c + 127) >> 7;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v2 = __shfl_up_sync(kAll, v, o), b2 = __shfl_up_sync(kAll, b, o);
+        if (lane >= o) { v += v2; b += b2; }
+      }
+      if (e0 + lane < p.E) {
+        first[e0 + lane + 1] = rows + v;
+        sf_first[e0 + lane + 1] = blocks + b;
+      }
+      rows += __shfl_sync(kAll, v, 31);
+      blocks += __shfl_sync(kAll, b, 31);
+    }
+    if (lane == 0) first[0] = sf_first[0] = 0;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= p.E; e += kPlanThreads) {
+      p.offsets[e] = first[e];
+      p.sf_offsets[e] = sf_first[e];
+    }
+  int* mine = cnt + warp * p.E;
+  for (int i = i0; i < i1; i += 32) {
+    const bool live = i + lane < i1;
+    const int e = live ? __ldg(p.ids + i + lane) : -1;
+    const bool in = e >= 0 && e < p.E;
+    const unsigned same = __match_any_sync(kAll, in ? e : -1);
+    const int rank = in ? mine[e] + __popc(same & ((1u << lane) - 1u)) : 0;
+    __syncwarp();
+    if (in && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    __syncwarp();
+    if (live) {
+      p.pos[i + lane] = in ? first[e] + rank : -1;
+      p.sf_row[i + lane] = in ? sf_first[e] * 128 + rank : -1;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ combine
+// y[t] = bf16(sum_j w[t, j] o[pos[t, j]]), fp32, j in order; 8 columns a thread.
+__global__ void __launch_bounds__(256) combine_kernel(const uint16_t* o, int64_t ldo, const int* pos, const float* w,
+                                                      int64_t T, int topk, int64_t H, uint16_t* y, int64_t ldy) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t cols = H >> 3, total = T * cols;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t t = i / cols;
+    const int64_t c = (i - t * cols) * 8;
+    float acc[8] = {};
+    for (int j0 = 0; j0 < topk; j0 += 8) {
+      uint4 v[8];
+      float s[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = j0 + j < topk ? __ldg(pos + t * topk + j0 + j) : -1;
+        s[j] = r >= 0 ? __ldg(w + t * topk + j0 + j) : 0.0f;
+        v[j] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(o + r * ldo + c)) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t u[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc[2 * k] = fmaf(s[j], __uint_as_float(u[k] << 16), acc[2 * k]);
+          acc[2 * k + 1] = fmaf(s[j], __uint_as_float(u[k] & 0xFFFF0000u), acc[2 * k + 1]);
+        }
+      }
+    }
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * k], acc[2 * k + 1]);
+      r[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(y + t * ldy + c) = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+}
+
+template <typename Key>
+fp8q_status launch_route(const RouteParams& p, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.T + 7) / 8)), block(p.T < 8 ? 32 * static_cast<unsigned>(p.T) : 256);
+  if (p.E <= 32) return launch_kernel(route_kernel<1, Key>, grid, block, 0, s, 1, p);
+  if (p.E <= 64) return launch_kernel(route_kernel<2, Key>, grid, block, 0, s, 1, p);
+  if (p.E <= 128) return launch_kernel(route_kernel<4, Key>, grid, block, 0, s, 1, p);
+  if (p.E <= 256) return launch_kernel(route_kernel<8, Key>, grid, block, 0, s, 1, p);
+  return launch_kernel(route_kernel<16, Key>, grid, block, 0, s, 1, p);
+}
+
+int64_t plan_blocks(int64_t n) { return n <= kPlanBlock ? 1 : (n + kPlanBlock - 1) / kPlanBlock; }
+
+// The pieces of the experts' workspace, each 256-byte aligned.
+struct ExpertsSpace {
+  size_t pos, sf_row, offsets, sf_offsets, hist, xq, xsf, hq, hsf, o, total;
+};
+ExpertsSpace experts_space(int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I, int format) {
+  ExpertsSpace w{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += (bytes + 255) / 256 * 256;
+    return r;
+  };
+  const int64_t R = T * topk, blocks = R / 128 + (R < E ? R : E);   // scale block rows: every expert's last may be ragged
+  w.pos = take(R * 4);
+  w.sf_row = take(R * 4);
+  w.offsets = take((E + 1) * 4);
+  w.sf_offsets = take((E + 1) * 4);
+  w.hist = take(fp8q_moe_plan_workspace_bytes(R, E));
+  w.xq = take(R * (H / 2));
+  w.xsf = take(blocks * fp4_kblocks(format, H) * 512);
+  w.hq = take(R * (I / 2));
+  w.hsf = take(blocks * fp4_kblocks(format, I) * 512);
+  w.o = take(R * H * 2);
+  w.total = at;
+  return w;
+}
+
+bool experts_sizes(int64_t T, int topk, int64_t E, int64_t H, int64_t I, int format) {
+  return (format == FP8Q_FP4_NV || format == FP8Q_FP4_MX) && T >= 0 && topk > 0 && topk <= kMaxTopk && E > 0 &&
+         E <= kMaxExperts && H > 0 && H % 32 == 0 && I > 0 && H <= (1 << 24) && I <= (1 << 24) &&
+         T * topk < (int64_t{1} << 30);
+}
+
+}  // namespace
+}  // namespace fp8q
+
+using namespace fp8q;
+
+extern "C" fp8q_status fp8q_moe_route(const void* logits, int logits_bf16, int64_t T, int64_t E, int64_t ldl, int topk,
+                                      int scoring, const float* bias, int num_groups, int topk_groups, int renormalize,
+                                      float scale, float* weights, int* ids, void* stream) {
+  if (T < 0 || E <= 0 || ldl < E || topk <= 0 || num_groups <= 0 || topk_groups <= 0) return FP8Q_ERR_INVALID_ARG;
+  if (logits_bf16 != 0 && logits_bf16 != 1) return FP8Q_ERR_INVALID_ARG;
+  if (scoring != FP8Q_ROUTE_SOFTMAX && scoring != FP8Q_ROUTE_SIGMOID) return FP8Q_ERR_INVALID_ARG;
+  if (renormalize != 0 && renormalize != 1) return FP8Q_ERR_INVALID_ARG;
+  if (E > kMaxExperts || topk > kMaxTopk || num_groups > 32) return FP8Q_ERR_UNSUPPORTED;
+  if (E % num_groups != 0 || topk_groups > num_groups || topk > E / num_groups * topk_groups) return FP8Q_ERR_INVALID_ARG;
+  if (T >= (int64_t{1} << 31)) return FP8Q_ERR_INVALID_ARG;
+  if (T == 0) return FP8Q_OK;
+  if (!logits || !weights || !ids) return FP8Q_ERR_INVALID_ARG;
+  if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(ids, 4))
+    return FP8Q_ERR_INVALID_ARG;
+  const RouteParams p{logits, T, ldl, static_cast<int>(E), logits_bf16, scoring == FP8Q_ROUTE_SIGMOID, bias, num_groups,
+                      topk_groups, topk, renormalize, scale, weights, ids};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return bias ? launch_route<uint64_t>(p, s) : launch_route<uint32_t>(p, s);
+}
+
+extern "C" size_t fp8q_moe_plan_workspace_bytes(int64_t n, int64_t E) {
+  if (n <= 0 || E <= 0) return 0;
+  const int64_t b = plan_blocks(n);
+  return b > 1 ? static_cast<size_t>(b) * static_cast<size_t>(E) * 4 : 0;
+}
+
+extern "C" fp8q_status fp8q_moe_plan(const int* ids, int64_t n, int64_t E, int* offsets, int* sf_offsets, int* pos,
+                                     int* sf_row, void* workspace, size_t ws_bytes, void* stream) {
+  if (n < 0 || E <= 0 || n >= (int64_t{1} << 30)) return FP8Q_ERR_INVALID_ARG;
+  if (E > kMaxExperts) return FP8Q_ERR_UNSUPPORTED;
+  if (!offsets || !sf_offsets || !aligned(offsets, 4) || !aligned(sf_offsets, 4)) return FP8Q_ERR_INVALID_ARG;
+  if (n > 0 && (!ids || !pos || !sf_row || !aligned(ids, 4) || !aligned(pos, 4) || !aligned(sf_row, 4)))
+    return FP8Q_ERR_INVALID_ARG;
+  const size_t need = fp8q_moe_plan_workspace_bytes(n, E);
+  if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 4))) return FP8Q_ERR_INVALID_ARG;
+  const int blocks = static_cast<int>(n > 0 ? plan_blocks(n) : 1);
+  const PlanParams p{ids, static_cast<int>(n), static_cast<int>(E), blocks, offsets, sf_offsets, pos, sf_row,
+                     static_cast<int*>(workspace)};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t smem = static_cast<size_t>(kPlanWarps) * static_cast<size_t>(E) * 4;   // at most 64 KB
+  static std::atomic<int> attr_done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8Q_ERR_CUDA;
+  if (!attr_done[dev].load(std::memory_order_relaxed)) {
+    for (auto k : {plan_count_kernel, plan_place_kernel})
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanWarps * kMaxExperts * 4) != cudaSuccess)
+        return FP8Q_ERR_CUDA;
+    attr_done[dev].store(1, std::memory_order_relaxed);
+  }
+  if (blocks > 1) {
+    const fp8q_status st = launch_kernel(plan_count_kernel, dim3(blocks), dim3(kPlanThreads), smem, s, 1, p);
+    if (st != FP8Q_OK) return st;
+  }
+  return launch_kernel(plan_place_kernel, dim3(blocks), dim3(kPlanThreads), smem, s, 1, p);
+}
+
+extern "C" fp8q_status fp8q_moe_combine(const void* o, int64_t ldo, const int* pos, const float* weights, int64_t T,
+                                        int topk, int64_t H, void* y, int64_t ldy, void* stream) {
+  if (T < 0 || topk <= 0 || H <= 0 || H % 8 != 0 || ldo < H || ldo % 8 != 0 || ldy < H || ldy % 8 != 0)
+    return FP8Q_ERR_INVALID_ARG;
+  if (T == 0) return FP8Q_OK;
+  if (!o || !pos || !weights || !y) return FP8Q_ERR_INVALID_ARG;
+  if (!aligned(o, 16) || !aligned(y, 16) || !aligned(pos, 4) || !aligned(weights, 4)) return FP8Q_ERR_INVALID_ARG;
+  const int64_t blocks = (T * (H >> 3) + 255) / 256, cap = static_cast<int64_t>(num_sms()) * 32;
+  return launch_kernel(combine_kernel, dim3(static_cast<unsigned>(blocks < cap ? blocks : cap)), dim3(256), 0,
+                       static_cast<cudaStream_t>(stream), 1, static_cast<const uint16_t*>(o), ldo, pos, weights, T, topk,
+                       H, static_cast<uint16_t*>(y), ldy);
+}
+
+extern "C" size_t fp8q_moe_experts_fp4_workspace_bytes(int64_t T, int topk, int64_t E, int64_t H, int64_t I, int format) {
+  if (!experts_sizes(T, topk, E, H, I, format) || T == 0) return 0;
+  return experts_space(T, topk, E, H, I, format).total;
+}
+
+extern "C" fp8q_status fp8q_moe_experts_fp4(const void* x, int64_t T, int64_t ldx, const int* ids, const float* weights,
+                                            int topk, int64_t E, int64_t H, int64_t I, int format, const void* w13,
+                                            const uint8_t* w13_sf, const void* w2, const uint8_t* w2_sf,
+                                            const float* x_gscale, const float* w13_gscale, const float* h_gscale,
+                                            const float* w2_gscale, void* y, int64_t ldy, void* workspace,
+                                            size_t ws_bytes, void* stream) {
+  if (!experts_sizes(T, topk, E, H, I, format)) return FP8Q_ERR_INVALID_ARG;
+  if (I % 128 != 0) return FP8Q_ERR_UNSUPPORTED;
+  if (ldx < H || ldx % 8 != 0 || ldy < H || ldy % 8 != 0) return FP8Q_ERR_INVALID_ARG;
+  if (format == FP8Q_FP4_MX && (x_gscale || w13_gscale || h_gscale || w2_gscale)) return FP8Q_ERR_INVALID_ARG;
+  if (T == 0) return FP8Q_OK;
+  if (!x || !ids || !weights || !w13 || !w13_sf || !w2 || !w2_sf || !y || !workspace) return FP8Q_ERR_INVALID_ARG;
+  const ExpertsSpace sp = experts_space(T, topk, E, H, I, format);
+  if (ws_bytes < sp.total || !aligned(workspace, 256)) return FP8Q_ERR_INVALID_ARG;
+  uint8_t* b = static_cast<uint8_t*>(workspace);
+  int* pos = reinterpret_cast<int*>(b + sp.pos);
+  int* sf_row = reinterpret_cast<int*>(b + sp.sf_row);
+  int* offsets = reinterpret_cast<int*>(b + sp.offsets);
+  int* sf_offsets = reinterpret_cast<int*>(b + sp.sf_offsets);
+  const int64_t R = T * topk;
+  // every argument is checked before the first launch: what the calls below would refuse
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(ids, 4) || !aligned(weights, 4) || !aligned(w13, 16) ||
+      !aligned(w13_sf, 16) || !aligned(w2, 16) || !aligned(w2_sf, 16) || !aligned(x_gscale, 4) ||
+      !aligned(w13_gscale, 4) || !aligned(h_gscale, 4) || !aligned(w2_gscale, 4))
+    return FP8Q_ERR_INVALID_ARG;
+  if (E * 2 * I >= (int64_t{1} << 31) || E * H >= (int64_t{1} << 31)) return FP8Q_ERR_INVALID_ARG;
+  fp8q_status st = fp8q_moe_plan(ids, R, E, offsets, sf_offsets, pos, sf_row, b + sp.hist, sp.xq - sp.hist, stream);
+  if (st != FP8Q_OK) return st;
+  st = fp8q_moe_fp4_quant(x, T, H, ldx, topk, pos, sf_row, format, x_gscale, b + sp.xq, H / 2, b + sp.xsf, stream);
+  if (st != FP8Q_OK) return st;
+  st = fp8q_grouped_mm_fp4_silu_quant(b + sp.xq, w13, b + sp.xsf, w13_sf, format, x_gscale, w13_gscale, offsets,
+                                      sf_offsets, E, R, I, H, h_gscale, b + sp.hq, b + sp.hsf, stream);
+  if (st != FP8Q_OK) return st;
+  st = fp8q_grouped_mm_fp4(b + sp.hq, w2, b + sp.hsf, w2_sf, format, h_gscale, w2_gscale, offsets, sf_offsets, E, R, H,
+                           I, b + sp.o, H, stream);
+  if (st != FP8Q_OK) return st;
+  return fp8q_moe_combine(b + sp.o, H, pos, weights, T, topk, H, y, ldy, stream);
+}
