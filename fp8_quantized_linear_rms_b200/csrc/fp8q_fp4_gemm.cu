@@ -67,7 +67,8 @@ struct Fp4Args {
 // registers; in code under elect.sync the compiler knows that one lane runs and
 // issues them directly, while under `lane == 0` it wraps each in a loop over
 // the warp's active lanes (measured: 64 against 18 cycles a tcgen05.cp, 109
-// against 59 a 64-column MMA).
+// against 59 a 64-column MMA).  The loops around it are run by the whole warp,
+// so that addresses and descriptors stay in uniform registers.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -79,24 +80,48 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // D[tmem] (+)= (A SFA)(B SFB)^T, both e2m1.
-template <int FMT>
+#define FP4_MMA(GROUP, KIND)                                                                                    \
+  asm volatile(                                                                                                 \
+      "{\n\t.reg .pred p;\n\t"                                                                                  \
+      "setp.ne.b32 p, %4, 0;\n\t"                                                                               \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d), "l"(a),  \
+      "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)                                                          \
+      : "memory")
+template <int FMT, bool PAIR>
 __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
                                         uint32_t sfa, uint32_t sfb) {
   if constexpr (FMT == kNv) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::
-            "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
-        : "memory");
+    if constexpr (PAIR) FP4_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    else FP4_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
   } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::
-            "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(sfa), "r"(sfb)
-        : "memory");
+    if constexpr (PAIR) FP4_MMA("2", "mxf4.block_scale.scale_vec::2X");
+    else FP4_MMA("1", "mxf4.block_scale.scale_vec::2X");
   }
+}
+#undef FP4_MMA
+
+// Arrive on the even CTA's barrier without releasing memory: what the MMAs wait
+// for is that tensor memory has been read, which tcgen05.wait::ld and the
+// tcgen05 fence order; a release at cluster scope would also wait for this
+// thread's stores to y (~1300 cycles a tile).
+__device__ __forceinline__ void arrive_relaxed(uint32_t bar_cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
+}
+
+// A 512-byte scale block -- 32 rows of 16 bytes, row l the scales of operand
+// rows l, l + 32, l + 64, l + 96 -- from shared memory into 4 columns of all
+// four lane quadrants of tensor memory (of both CTAs, each from its own shared
+// memory, for a pair).  Descriptor: K-major, no swizzle, 8-row core matrices
+// 128 bytes apart, version 1.  A thread's copies and MMAs run in issue order.
+__device__ __forceinline__ uint64_t scales_desc(const void* src) {
+  return (static_cast<uint64_t>(smem_u32(src) & 0x3FFFF) >> 4) | (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
+}
+template <bool PAIR>
+__device__ __forceinline__ void cp_scales(uint32_t col, uint64_t desc) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(col), "l"(desc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(col), "l"(desc) : "memory");
 }
 
 // Instruction descriptor of the 4-bit block-scaled kinds: scale id of B (bits
@@ -125,7 +150,9 @@ struct Fp4Tile {
 // Tile u: an expert's tiles are consecutive, its token tiles the fastest index
 // (they share the weight tile, which then comes from L2).  pre[e]: token tiles
 // before expert e.
-__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const int* pre, int u, int tn) {
+// A CTA pair's tile has 256 token rows; `rank` says which 128 of them.
+template <bool PAIR>
+__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const int* pre, int u, int tn, int rank) {
   Fp4Tile t;
   int lo = 0, hi = p.E;
   while (hi - lo > 1) {
@@ -138,9 +165,10 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const int* pre, in
   const int64_t first = p.offsets ? p.offsets[lo] : 0;
   const int64_t end = p.offsets ? p.offsets[lo + 1] : p.M;
   t.e = lo;
-  t.t0 = first + 128 * m;
-  t.cnt = static_cast<int>(min(static_cast<int64_t>(128), end - t.t0));
-  t.tblk = (p.sf_offsets ? p.sf_offsets[lo] : 0) + m;
+  const int b = PAIR ? 2 * m + rank : m;
+  t.t0 = first + 128 * static_cast<int64_t>(b);
+  t.cnt = static_cast<int>(max(int64_t{0}, min(int64_t{128}, end - t.t0)));
+  t.tblk = (p.sf_offsets ? p.sf_offsets[lo] : 0) + b;
   t.n0 = static_cast<int64_t>(nt) * tn;
   return t;
 }
@@ -149,8 +177,14 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const int* pre, in
 // CH output columns a tile: 64, 128 or 256 weight rows, or FUSED 64 or 128
 // hidden channels, whose gate rows are followed by the up rows.  128 channels
 // are one 256-column MMA, 64 are two 64-column ones (gate, up), each with the
-// scale block that its rows lie in.
-template <int FMT, int CH, bool FUSED>
+// scale block that its rows lie in.  PAIR: two CTAs of a cluster share one MMA
+// of 256 token rows and 256 columns (tcgen05 cta_group::2), each with 128 of
+// the rows of both operands in its shared memory, so a weight row reaches each
+// SM half as often; each holds the scales of its own tokens and of all columns.
+// Tried and slower: a tile as two 128-column MMAs and accumulators, so that one
+// is read while the other computes (a pair's 128-column MMA took ~140 cycles,
+// more than the 256-column one: 1341 against 894 us at 8192 x 51200 x 5120).
+template <int FMT, int CH, bool FUSED, bool PAIR>
 struct Fp4Cfg {
   static constexpr bool SMALL = CH == 64;                   // two CTAs on an SM
   static constexpr int BN = FUSED ? 2 * CH : CH;            // accumulator columns
@@ -163,22 +197,27 @@ struct Fp4Cfg {
   static constexpr int SF_COLS = NKB * 4;
   static constexpr int BBLK = FUSED || BN == 256 ? 2 : 1;   // 128-row blocks of weight scales
   static constexpr int BBOX = FUSED ? CH : (BN < 128 ? BN : 128);   // weight rows of one copy
-  static constexpr int B_BYTES = BN * kStageBytes;
+  static constexpr int B_BYTES = (PAIR ? 128 : BN) * kStageBytes;
   static constexpr int SF_STAGE = (1 + BBLK) * SF_BYTES;
   static constexpr int SF_TMEM = (1 + BBLK) * SF_COLS;      // tensor memory columns of a stage's scales
   static constexpr int SFBUF = SMALL ? 2 : 4;
-  static constexpr int NBUF = BN == 256 || TWO_MMA ? 1 : 2; // accumulator buffers
+  static constexpr int NBUF = BN == 256 || TWO_MMA ? 1 : 2; // accumulators
   static constexpr int ACC_COLS = NBUF * BN;
   static constexpr int TMEM = SMALL ? 256 : 512;
-  static constexpr int B_STEP = TWO_MMA ? 4 : 4 * BBLK;     // scale columns from one K block to the next
+  // tensor memory columns of the weight scales: from one K block to the next, and between their
+  // 128-row blocks (side by side for one 256-column MMA)
+  static constexpr int B_STEP = MMA_N == 256 ? 8 : 4;
+  static constexpr int B_BLOCK = MMA_N == 256 ? 4 : SF_COLS;
   static_assert(ACC_COLS + SFBUF * SF_TMEM + 4 <= TMEM, "tensor memory");
+  static_assert(!PAIR || BN == 256, "pairs have 256 columns");
 };
 
-template <int FMT, int CH, bool FUSED>
-__global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, CH, FUSED>::SMALL ? 2 : 1)
+template <int FMT, int CH, bool FUSED, bool PAIR>
+__global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<FMT, CH, FUSED, PAIR>::SMALL ? 2 : 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmW,
+                    const __grid_constant__ CUtensorMap tmTS, const __grid_constant__ CUtensorMap tmWS,
                     const Fp4Args p) {
-  using C = Fp4Cfg<FMT, CH, FUSED>;
+  using C = Fp4Cfg<FMT, CH, FUSED, PAIR>;
   constexpr int BN = C::BN, NB = C::NBUF;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int pre[kMaxExperts + 1];
@@ -197,6 +236,9 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, C
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int cta = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);    // of the tile loop
+  const int ctas = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -205,7 +247,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, C
     }
     for (int i = 0; i < NB; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], C::EPI_WARPS);
+      mbar_init(&tempty[i], C::EPI_WARPS * (PAIR ? 2 : 1));
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -216,21 +258,27 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, C
     prefetch_tmap(&tmW);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::TMEM);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, C::TMEM);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::TMEM);
+      tmem_relinquish();
+    }
   }
   griddep_wait();
   griddep_launch_dependents();
 
   // pre[e]: token tiles before expert e
+  constexpr int kTM = PAIR ? 256 : 128;
   if (p.offsets == nullptr) {
     if (threadIdx.x == 0) {
       pre[0] = 0;
-      pre[1] = static_cast<int>((p.M + 127) / 128);
+      pre[1] = static_cast<int>((p.M + kTM - 1) / kTM);
     }
   } else {
     for (int e = threadIdx.x; e < p.E; e += C::THREADS)
-      pre[e + 1] = (p.offsets[e + 1] - p.offsets[e] + 127) / 128;
+      pre[e + 1] = (p.offsets[e + 1] - p.offsets[e] + kTM - 1) / kTM;
     if (threadIdx.x == 0) pre[0] = 0;
     __syncthreads();
     if (warp == 0) {
@@ -250,100 +298,150 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, C
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();      // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int units = pre[p.E] * p.tiles_n;
 
+  // a wait by the whole warp; false in all lanes if one gave up
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.status)) != 0;
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (elect_one()) {
-      int it = 0;
+    {
+      int it = 0, st = 0;
+      uint32_t parity = 1;
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
-        const Fp4Tile t = fp4_tile(p, pre, u, CH);
+      for (int u = cta; ok && u < units; u += ctas) {
+        const Fp4Tile t = fp4_tile<PAIR>(p, pre, u, CH, rank);
         const int wrow = static_cast<int>(t.e * p.N + t.n0);
-        const int up = FUSED ? static_cast<int>(p.I) : 128;       // from the first copy's rows to the second's
+        const int up = FUSED ? static_cast<int>(p.I) : 128;       // from the first 128 weight rows to the second
         const int pieces = (t.cnt + p.box - 1) / p.box;
+        const int64_t wblk = t.e * p.wblocks + (t.n0 >> 7);
         const uint8_t* sft = p.sft + t.tblk * p.kb * 512;
-        const uint8_t* sfw = p.sfw + (t.e * p.wblocks + (t.n0 >> 7)) * p.kb * 512;
+        const uint8_t* sfw = p.sfw + wblk * p.kb * 512;
         // a second block of weight scales: the up half's, or columns 128..255
         const int64_t second = static_cast<int64_t>(up >> 7) * p.kb * 512;
         const bool two = FUSED || (BN == 256 && t.n0 + 128 < p.N);
-        for (int kb = 0; kb < p.kstages; ++kb, ++it) {
-          const int st = it % S;
-          if (!mbar_wait(&empty[st], ((it / S) & 1) ^ 1u, abort_flag, p.status)) { ok = false; break; }
-          const uint32_t sfb = min(C::NKB, p.kb - kb * C::NKB) * 512;
-          const int64_t sfo = static_cast<int64_t>(kb) * C::SF_BYTES;
-          mbar_arrive_expect_tx(&full[st], pieces * p.box * kStageBytes + C::B_BYTES + (two ? 3 : 2) * sfb);
+        int pair_pieces = 0;                                      // of both CTAs, and which have token scales
+        if constexpr (PAIR) {
+          const int other = rank ? 128 : max(0, fp4_tile<PAIR>(p, pre, u, CH, 1).cnt);
+          pair_pieces = pieces + (other + p.box - 1) / p.box;
+        }
+        for (int kb = 0; kb < p.kstages; ++kb) {
+          if (!warp_wait(&empty[st], parity)) { ok = false; break; }
           uint8_t* a = sA + st * p.a_bytes;
           uint8_t* b = sB + st * C::B_BYTES;
           uint8_t* s = sSF + st * C::SF_STAGE;
           const int x = kb * kStageBytes;
-          tma_load_2d(b, &tmW, &full[st], x, wrow);
-          if (C::BBLK == 2) tma_load_2d(b + C::BBOX * kStageBytes, &tmW, &full[st], x, wrow + up);
-          bulk_load(s + C::SF_BYTES, sfw + sfo, sfb, &full[st]);
-          if (two) bulk_load(s + 2 * C::SF_BYTES, sfw + second + sfo, sfb, &full[st]);
-          for (int i = 0; i < pieces; ++i)
-            tma_load_2d(a + i * p.box * kStageBytes, &tmT, &full[st], x, static_cast<int>(t.t0) + i * p.box);
-          bulk_load(s, sft + sfo, sfb, &full[st]);
+          if (elect_one()) {
+            if constexpr (PAIR) {
+              // everything lands on the even CTA's barrier; boxes reaching past a matrix count in full
+              if (rank == 0)
+                mbar_arrive_expect_tx(&full[st], pair_pieces * p.box * kStageBytes + 2 * C::B_BYTES + 6 * C::SF_BYTES);
+              const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
+              const int y = kb * C::NKB;
+              tma_load_2d_pair(b, &tmW, bar, x, wrow + (rank ? up : 0));
+              tma_load_2d_pair(s + C::SF_BYTES, &tmWS, bar, 0, static_cast<int>(wblk) * p.kb + y);
+              tma_load_2d_pair(s + 2 * C::SF_BYTES, &tmWS, bar, 0, static_cast<int>(wblk + (up >> 7)) * p.kb + y);
+              for (int i = 0; i < pieces; ++i)
+                tma_load_2d_pair(a + i * p.box * kStageBytes, &tmT, bar, x, static_cast<int>(t.t0) + i * p.box);
+              tma_load_2d_pair(s, &tmTS, bar, 0, static_cast<int>(t.tblk) * p.kb + y);
+            } else {
+              const uint32_t sfb = min(C::NKB, p.kb - kb * C::NKB) * 512;
+              const int64_t sfo = static_cast<int64_t>(kb) * C::SF_BYTES;
+              mbar_arrive_expect_tx(&full[st], pieces * p.box * kStageBytes + C::B_BYTES + (two ? 3 : 2) * sfb);
+              tma_load_2d(b, &tmW, &full[st], x, wrow);
+              if (C::BBLK == 2) tma_load_2d(b + C::BBOX * kStageBytes, &tmW, &full[st], x, wrow + up);
+              bulk_load(s + C::SF_BYTES, sfw + sfo, sfb, &full[st]);
+              if (two) bulk_load(s + 2 * C::SF_BYTES, sfw + second + sfo, sfb, &full[st]);
+              for (int i = 0; i < pieces; ++i)
+                tma_load_2d(a + i * p.box * kStageBytes, &tmT, &full[st], x, static_cast<int>(t.t0) + i * p.box);
+              bulk_load(s, sft + sfo, sfb, &full[st]);
+            }
+          }
+          __syncwarp();
+          ++it;
+          if (++st == S) { st = 0; parity ^= 1u; }
         }
       }
-      // after a wait that gave up: let the copies in flight land
+      // let the copies in flight land before this CTA (or its pair) can leave;
+      // at once when everything was consumed
       const int first = it - S > 0 ? it - S : 0;
-      for (int j = first; !ok && j < it; ++j) drain_wait(&full[j % S], (j / S) & 1);
+      for (int j = first; (PAIR ? rank == 0 : !ok) && j < it; ++j) drain_wait(&full[j % S], (j / S) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (elect_one()) {
-      const uint32_t id0 = idesc_fp4(FMT, 128, C::MMA_N, 0);
-      int it = 0, tc = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++tc) {
-        // 64-column tiles: the second half of a 128-row scale block lies two columns on
-        const uint32_t wcol = C::SMALL ? static_cast<uint32_t>((fp4_tile(p, pre, u, CH).n0 & 64) >> 5) : 0u;
-        const int buf = tc % NB;
-        if (!mbar_wait(&tempty[buf], ((tc / NB) & 1) ^ 1u, abort_flag, p.status)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d = tmem + buf * BN;
-        for (int kb = 0; kb < p.kstages; ++kb, ++it) {
-          const int st = it % S;
-          if (!mbar_wait(&full[st], (it / S) & 1, abort_flag, p.status)) { ok = false; break; }
+    // ------------------------------------------------------------ MMA issuer (the even CTA's, of a pair)
+    {
+      if (rank == 0) {
+        const uint32_t id0 = idesc_fp4(FMT, PAIR ? 256 : 128, C::MMA_N, 0);
+        auto commit = [](uint64_t* bar) {
+          if constexpr (PAIR) mma_commit_pair(bar, 0x3);
+          else mma_commit(bar);
+        };
+        const uint64_t a_desc = smem_desc_kmajor_sw128(sA), b_desc = smem_desc_kmajor_sw128(sB);
+        const uint64_t sf_desc = scales_desc(sSF);
+        int st = 0, sbuf = 0, buf = 0;
+        uint32_t parity = 0, acc_parity = 1;
+        bool ok = true;
+        for (int u = cta; ok && u < units; u += ctas) {
+          // 64-column tiles: the second half of a 128-row scale block lies two columns on
+          const uint32_t wcol =
+              C::SMALL ? static_cast<uint32_t>((fp4_tile<PAIR>(p, pre, u, CH, 0).n0 & 64) >> 5) : 0u;
+          if (!warp_wait(&tempty[buf], acc_parity)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sfa = tmem + C::ACC_COLS + (it % C::SFBUF) * C::SF_TMEM;
-          const uint32_t sfb = sfa + C::SF_COLS;
-          const uint8_t* s = sSF + st * C::SF_STAGE;
-          const int nk = min(C::NKB, p.kb - kb * C::NKB);
-          for (int b = 0; b < nk; ++b) {
-            tmem_cp_sf_chunk(sfa + b * 4, s + b * 512);
+          for (int kb = 0; kb < p.kstages; ++kb) {
+            if (!warp_wait(&full[st], parity)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sfa = tmem + C::ACC_COLS + sbuf * C::SF_TMEM;
+            const uint32_t sfb = sfa + C::SF_COLS + wcol;
+            const uint64_t sd = sf_desc + static_cast<uint32_t>(st * (C::SF_STAGE >> 4));
+            const uint64_t ad = a_desc + static_cast<uint32_t>(st * (p.a_bytes >> 4));
+            const uint64_t bd = b_desc + static_cast<uint32_t>(st * (C::B_BYTES >> 4));
+            const int nk = p.kb - kb * C::NKB;                       // scale blocks and K slices left
+            const int ks = static_cast<int>((p.K - static_cast<int64_t>(kb) * 256 + 63) >> 6);
+            // the stage's MMAs into columns d: weight rows from descriptor w on, their scales at column sw
+            auto mmas = [&](uint32_t d, uint64_t w, uint32_t sw) {
 #pragma unroll
-            for (int j = 0; j < C::BBLK; ++j)
-              tmem_cp_sf_chunk(sfb + b * C::B_STEP + j * (C::TWO_MMA ? C::SF_COLS : 4),
-                               s + (1 + j) * C::SF_BYTES + b * 512);
+              for (int k = 0; k < 4; ++k) {
+                if (k < ks) {
+                  // nvfp4: a K slice has a scale block of its own; mxfp4: two share one, ids 0 and 2
+                  const int b = FMT == kNv ? k : k >> 1;
+                  const uint32_t id = FMT == kNv ? 0u : 2u * (k & 1);
+                  mma_fp4<FMT, PAIR>(d, ad + 2 * k, w + 2 * k, id0 | (id << 4) | (id << 29), kb > 0 || k > 0,
+                                     (sfa + b * 4) | (id << 30), (sw + b * C::B_STEP) | (id << 30));
+                }
+              }
+            };
+            if (elect_one()) {
+#pragma unroll
+              for (int b = 0; b < C::NKB; ++b) {
+                if (b < nk) {
+                  cp_scales<PAIR>(sfa + b * 4, sd + (b * 512 >> 4));
+#pragma unroll
+                  for (int j = 0; j < C::BBLK; ++j)
+                    cp_scales<PAIR>(sfa + C::SF_COLS + b * C::B_STEP + j * C::B_BLOCK,
+                                    sd + (((1 + j) * C::SF_BYTES + b * 512) >> 4));
+                }
+              }
+              const uint32_t d = tmem + buf * BN;
+              mmas(d, bd, sfb);
+              if constexpr (C::TWO_MMA) mmas(d + CH, bd + (CH * kStageBytes >> 4), sfb + C::B_BLOCK);
+              commit(&empty[st]);
+              if (kb + 1 == p.kstages) commit(&tfull[buf]);
+            }
+            __syncwarp();
+            if (++st == S) { st = 0; parity ^= 1u; }
+            if (++sbuf == C::SFBUF) sbuf = 0;
           }
-          const uint64_t ad = smem_desc_kmajor_sw128(sA + st * p.a_bytes);
-          const uint64_t bd = smem_desc_kmajor_sw128(sB + st * C::B_BYTES);
-          const int64_t left = p.K - static_cast<int64_t>(kb) * 256;
-          const int ks = left >= 256 ? 4 : static_cast<int>((left + 63) >> 6);
-#pragma unroll 4
-          for (int k = 0; k < ks; ++k) {
-            // nvfp4: a K slice has a scale block of its own; mxfp4: two share one, ids 0 and 2
-            const int b = FMT == kNv ? k : k >> 1;
-            const uint32_t id = FMT == kNv ? 0u : 2u * (k & 1);
-            const uint32_t idesc = id0 | (id << 4) | (id << 29);
-            const uint32_t sa = (sfa + b * 4) | (id << 30);
-            const uint32_t sb = (sfb + b * C::B_STEP + wcol) | (id << 30);
-            mma_fp4<FMT>(d, ad + 2 * k, bd + 2 * k, idesc, kb > 0 || k > 0, sa, sb);
-            if constexpr (C::TWO_MMA)
-              mma_fp4<FMT>(d + CH, ad + 2 * k, bd + (CH * kStageBytes >> 4) + 2 * k, idesc, kb > 0 || k > 0, sa,
-                           sb + C::SF_COLS);
-          }
-          mma_commit(&empty[st]);
+          if (++buf == NB) { buf = 0; acc_parity ^= 1u; }
         }
-        if (ok) mma_commit(&tfull[buf]);
+        // every MMA issued has completed once `drain` flips
+        if (elect_one()) commit(drain);
       }
-      // every MMA issued has completed once `drain` flips
-      mma_commit(drain);
       drain_wait(drain, 0);
     }
     __syncwarp();
@@ -356,37 +454,47 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, C
     const float gh = FUSED && p.gh ? *p.gh : 1.0f;
     constexpr int COLS = CH / (C::EPI_WARPS / 4);     // output columns of a thread
     const int col0 = ((warp - 2) >> 2) * COLS;
-    int tc = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++tc) {
-      const Fp4Tile t = fp4_tile(p, pre, u, CH);
-      const float alpha = p.gb ? ga * p.gb[t.e] : ga;
-      const int buf = tc % NB;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[buf], (tc / NB) & 1, abort_flag, p.status))) {
-        ok = false;
-        break;
+    const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
+    // the accumulator goes back to the MMAs (of the even CTA)
+    auto give_back = [&](int buf) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) arrive_relaxed(tempty0 + 8u * buf);
+        else mbar_arrive(&tempty[buf]);
       }
-      tc_fence_after();
-      const uint32_t acc = tmem + lane_addr + buf * BN + col0;
-      const int64_t n = t.n0 + col0;
+    };
+    int buf = 0;
+    uint32_t parity = 0;
+    bool ok = true;
+    for (int u = cta; ok && u < units; u += ctas) {
+      const Fp4Tile t = fp4_tile<PAIR>(p, pre, u, CH, rank);
+      const float alpha = p.gb ? ga * p.gb[t.e] : ga;
       if constexpr (!FUSED) {
-        // The thread's columns, rounded to bf16 as they are read, so that the
-        // accumulator goes back to the MMAs before anything is stored.
+        if (!warp_wait(&tfull[buf], parity)) { ok = false; break; }
+        tc_fence_after();
+        // The thread's columns, rounded to bf16 as they are read (the next 32 in
+        // flight meanwhile), so that the accumulator goes back to the MMAs
+        // before anything is stored.
         uint32_t o[COLS / 2];
         if (quad * 32 < t.cnt) {
+          const uint32_t acc = tmem + lane_addr + buf * BN + col0;
+          uint32_t v[2][32];
+          tmem_ld_async<32>(acc, v[0]);
 #pragma unroll
           for (int c = 0; c < COLS; c += 32) {
-            uint32_t v[32];
-            tmem_ld_waited<32>(acc + c, v);
+            uint32_t* w = v[(c / 32) & 1];
+            tmem_wait_regs<32>(w);
+            if (c + 32 < COLS) tmem_ld_async<32>(acc + c + 32, v[(c / 32 + 1) & 1]);
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
-              o[(c + i) / 2] = pack_bf16(__uint_as_float(v[i]) * alpha, __uint_as_float(v[i + 1]) * alpha);
+              o[(c + i) / 2] = pack_bf16(__uint_as_float(w[i]) * alpha, __uint_as_float(w[i + 1]) * alpha);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[buf]);
+        give_back(buf);
+        if (++buf == NB) { buf = 0; parity ^= 1u; }
         if (r < t.cnt) {
+          const int64_t n = t.n0 + col0;
           uint16_t* y = p.y + (t.t0 + r) * p.ldy + n;
           if (p.vec32 && n + COLS <= p.N) {
 #pragma unroll
@@ -405,6 +513,11 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, C
       } else {
         // The same gate and up columns of the thread's row; the accumulator
         // goes back once they are in registers.
+        if (!warp_wait(&tfull[0], parity)) { ok = false; break; }
+        parity ^= 1u;
+        tc_fence_after();
+        const uint32_t acc = tmem + lane_addr + col0;
+        const int64_t n = t.n0 + col0;
         uint32_t g[COLS], w[COLS];
         if (quad * 32 < t.cnt) {
 #pragma unroll
@@ -418,9 +531,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, C
             tmem_wait_regs<32>(w + c);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[buf]);
+        give_back(0);
         if (r < t.cnt) {
           constexpr int G = fp4_group<FMT>();
           uint32_t code[COLS / 8], sfw = 0;
@@ -453,8 +564,12 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED>::THREADS, Fp4Cfg<FMT, C
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();      // neither leaves while the other may use its memory
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, C::TMEM);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, C::TMEM);
+    else tmem_dealloc(tmem, C::TMEM);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -490,16 +605,37 @@ bool fp4_tensor_map(const void* ptr, int64_t rows, int64_t K, int box_rows, CUte
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale blocks as rows of 512 bytes; box = `rows` blocks.
+bool fp4_scale_map(const void* ptr, int64_t blocks, int rows, CUtensorMap* out) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t gdim[2] = {128, static_cast<cuuint64_t>(blocks)};
+  const cuuint64_t gstride[1] = {512};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(rows)};
+  const cuuint32_t estride[2] = {1, 1};
+  return fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(ptr), gdim, gstride, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kStaticSmem = 4 * (kMaxExperts + 1) + 12;
 constexpr int kSmemMax = 227 * 1024 - kStaticSmem;
 constexpr int kSmemHalf = 113 * 1024 - kStaticSmem;   // two CTAs in 228 KB, 1 KB of each reserved
 
-template <int FMT, int CH, bool FUSED>
+template <int FMT, int CH, bool FUSED, bool PAIR>
 fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p, cudaStream_t stream) {
-  using C = Fp4Cfg<FMT, CH, FUSED>;
-  CUtensorMap mt, mw;
+  using C = Fp4Cfg<FMT, CH, FUSED, PAIR>;
+  CUtensorMap mt, mw, mts, mws;
   if (!fp4_tensor_map(t, p.M, p.K, p.box, &mt) || !fp4_tensor_map(w, p.E * p.N, p.K, C::BBOX, &mw))
     return FP8Q_ERR_CUDA;
+  if (PAIR) {
+    const int64_t tblocks = p.offsets ? p.M / 128 + (p.M < p.E ? p.M : p.E) : (p.M + 127) / 128;
+    if (!fp4_scale_map(p.sft, tblocks * p.kb, C::NKB, &mts) || !fp4_scale_map(p.sfw, p.E * p.wblocks * p.kb, C::NKB, &mws))
+      return FP8Q_ERR_CUDA;
+  } else {
+    mts = mt;      // not read
+    mws = mw;
+  }
   p.tiles_n = static_cast<int>(((FUSED ? p.I : p.N) + CH - 1) / CH);
   // A tile that is known to have fewer rows keeps less of them; its MMA reads
   // 128 rows' worth of shared memory from the tile's start all the same, so
@@ -511,18 +647,33 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
   p.stages = (budget - slack) / stage;
   if (p.stages > 12) p.stages = 12;
   const int smem = p.stages * stage + slack;
-  auto kern = fp4_gemm_kernel<FMT, CH, FUSED>;
-  static std::atomic<int> attr_done[64];
+  auto kern = fp4_gemm_kernel<FMT, CH, FUSED, PAIR>;
+  static std::atomic<int> attr_done[64];     // pairs: clusters that fit the device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8Q_ERR_CUDA;
-  if (!attr_done[dev].load(std::memory_order_relaxed)) {
+  int fit = attr_done[dev].load(std::memory_order_relaxed);
+  if (!fit) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, budget) != cudaSuccess)
       return FP8Q_ERR_CUDA;
-    attr_done[dev].store(1, std::memory_order_relaxed);
+    fit = num_sms() * (C::SMALL ? 2 : 1);
+    if (PAIR) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.gridDim = dim3(2 * static_cast<unsigned>(num_sms()));
+      cfg.blockDim = dim3(C::THREADS);
+      cfg.dynamicSmemBytes = smem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) != cudaSuccess || fit < 1) return FP8Q_ERR_CUDA;
+    }
+    attr_done[dev].store(fit, std::memory_order_relaxed);
   }
-  const int64_t units = tiles_t * p.tiles_n, slots = static_cast<int64_t>(num_sms()) * (C::SMALL ? 2 : 1);
-  const unsigned grid = static_cast<unsigned>(units < slots ? units : slots);
-  return launch_kernel(kern, dim3(grid), dim3(C::THREADS), smem, stream, 1, mt, mw, p);
+  const int64_t units = tiles_t * p.tiles_n;
+  const unsigned grid = static_cast<unsigned>(units < fit ? units : fit) * (PAIR ? 2 : 1);
+  return launch_kernel(kern, dim3(grid), dim3(C::THREADS), smem, stream, PAIR ? 2 : 1, mt, mw, mts, mws, p);
 }
 
 // Variant and launch.
@@ -534,12 +685,14 @@ fp8q_status run_fp4(const void* t, const void* w, Fp4Args& p, cudaStream_t strea
   p.box = per > 64 ? 128 : p.M <= 16 ? 16 : 32;
   const int64_t nw = FUSED ? p.I : p.N, sms = num_sms();
   if constexpr (FUSED) {
-    if (tt * (nw / 128) < sms) return launch_fp4<FMT, 64, true>(t, w, tt, p, stream);
-    return launch_fp4<FMT, 128, true>(t, w, tt, p, stream);
+    if (tt * (nw / 128) < sms) return launch_fp4<FMT, 64, true, false>(t, w, tt, p, stream);
+    return launch_fp4<FMT, 128, true, false>(t, w, tt, p, stream);
   } else {
-    if (per <= 64 || tt * ((nw + 127) / 128) < sms) return launch_fp4<FMT, 64, false>(t, w, tt, p, stream);
-    if (tt * ((nw + 255) / 256) < sms) return launch_fp4<FMT, 128, false>(t, w, tt, p, stream);
-    return launch_fp4<FMT, 256, false>(t, w, tt, p, stream);
+    if (per <= 64 || tt * ((nw + 127) / 128) < sms) return launch_fp4<FMT, 64, false, false>(t, w, tt, p, stream);
+    if (!p.offsets && ((p.M + 255) / 256) * ((nw + 255) / 256) >= sms / 2)
+      return launch_fp4<FMT, 256, false, true>(t, w, (p.M + 255) / 256, p, stream);
+    if (tt * ((nw + 255) / 256) < sms) return launch_fp4<FMT, 128, false, false>(t, w, tt, p, stream);
+    return launch_fp4<FMT, 256, false, false>(t, w, tt, p, stream);
   }
 }
 
