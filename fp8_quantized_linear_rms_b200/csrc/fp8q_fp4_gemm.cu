@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cstdlib>
 #include <mutex>
 
 #include "fp8q_common.cuh"
@@ -59,7 +60,6 @@ struct Fp4Args {
   int box;                     // token rows of one copy (16, 32, 128)
   int stages;
   int a_bytes;                 // shared memory of a stage's token tile
-  int vec32;                   // y may be written 32 bytes at a time
   int* status;
 };
 
@@ -141,34 +141,40 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // token scales' block row, and the first weight row (of the expert).
 struct Fp4Tile {
   int e;
-  int64_t t0;
+  int t0;
   int cnt;
   int64_t tblk;
   int64_t n0;
 };
 
+// What a CTA keeps of an expert in shared memory (read once, so that a tile
+// costs no loads from global memory): token tiles before it, its first row,
+// its rows, and the first block row of its scales.
+struct Fp4Expert {
+  int tiles, first, rows, sf;
+};
+
 // Tile u: an expert's tiles are consecutive, its token tiles the fastest index
-// (they share the weight tile, which then comes from L2).  pre[e]: token tiles
-// before expert e.
-// A CTA pair's tile has 256 token rows; `rank` says which 128 of them.
+// (they share the weight tile, which then comes from L2).  A CTA pair's tile
+// has 256 token rows; `rank` says which 128 of them.
 template <bool PAIR>
-__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const int* pre, int u, int tn, int rank) {
-  Fp4Tile t;
+__device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const Fp4Expert* ex, int u, int tn, int rank) {
+  constexpr int TM = PAIR ? 256 : 128;
   int lo = 0, hi = p.E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (static_cast<int64_t>(pre[mid]) * p.tiles_n <= u) lo = mid; else hi = mid;
+    if (ex[mid].tiles * p.tiles_n <= u) lo = mid; else hi = mid;
   }
-  const int mt = pre[lo + 1] - pre[lo];
-  const int r = u - pre[lo] * p.tiles_n;
-  const int nt = r / mt, m = r - nt * mt;
-  const int64_t first = p.offsets ? p.offsets[lo] : 0;
-  const int64_t end = p.offsets ? p.offsets[lo + 1] : p.M;
-  t.e = lo;
+  const Fp4Expert x = ex[lo];
+  const int mt = (x.rows + TM - 1) / TM;
+  const int r = u - x.tiles * p.tiles_n;
+  const int nt = mt == 1 ? r : r / mt, m = r - nt * mt;
   const int b = PAIR ? 2 * m + rank : m;
-  t.t0 = first + 128 * static_cast<int64_t>(b);
-  t.cnt = static_cast<int>(max(int64_t{0}, min(int64_t{128}, end - t.t0)));
-  t.tblk = (p.sf_offsets ? p.sf_offsets[lo] : 0) + b;
+  Fp4Tile t;
+  t.e = lo;
+  t.t0 = x.first + 128 * b;
+  t.cnt = max(0, min(128, x.rows - 128 * b));
+  t.tblk = x.sf + b;
   t.n0 = static_cast<int64_t>(nt) * tn;
   return t;
 }
@@ -204,6 +210,8 @@ struct Fp4Cfg {
   static constexpr int NBUF = BN == 256 || TWO_MMA ? 1 : 2; // accumulators
   static constexpr int ACC_COLS = NBUF * BN;
   static constexpr int TMEM = SMALL ? 256 : 512;
+  static constexpr bool STAGED = !FUSED && !SMALL;          // y leaves through shared memory
+  static constexpr int OUT_BYTES = STAGED ? EPI_WARPS * 4096 : 0;
   // tensor memory columns of the weight scales: from one K block to the next, and between their
   // 128-row blocks (side by side for one 256-column MMA)
   static constexpr int B_STEP = MMA_N == 256 ? 8 : 4;
@@ -220,20 +228,22 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
   using C = Fp4Cfg<FMT, CH, FUSED, PAIR>;
   constexpr int BN = C::BN, NB = C::NBUF;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int pre[kMaxExperts + 1];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const int S = p.stages;
   uint8_t* sA = smem;
   uint8_t* sB = sA + S * p.a_bytes;
   uint8_t* sSF = sB + S * C::B_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sSF + S * C::SF_STAGE);
+  uint8_t* sOut = sSF + S * C::SF_STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::OUT_BYTES);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
   uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* drain = full + 30;        // 16-byte aligned, whatever S <= 12
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* all_tiles = reinterpret_cast<int*>(tmem_slot + 2);
+  Fp4Expert* ex = reinterpret_cast<Fp4Expert*>(drain + 4);              // [E]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
@@ -269,39 +279,36 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
   griddep_wait();
   griddep_launch_dependents();
 
-  // pre[e]: token tiles before expert e
   constexpr int kTM = PAIR ? 256 : 128;
   if (p.offsets == nullptr) {
     if (threadIdx.x == 0) {
-      pre[0] = 0;
-      pre[1] = static_cast<int>((p.M + kTM - 1) / kTM);
+      ex[0] = {0, 0, static_cast<int>(p.M), 0};
+      *all_tiles = static_cast<int>((p.M + kTM - 1) / kTM);
     }
-  } else {
-    for (int e = threadIdx.x; e < p.E; e += C::THREADS)
-      pre[e + 1] = (p.offsets[e + 1] - p.offsets[e] + kTM - 1) / kTM;
-    if (threadIdx.x == 0) pre[0] = 0;
-    __syncthreads();
-    if (warp == 0) {
-      int carry = 0;
-      for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        int v = e < p.E ? pre[e + 1] : 0;
+  } else if (warp == 0) {
+    int carry = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int first = e < p.E ? __ldg(p.offsets + e) : 0;
+      const int rows = e < p.E ? __ldg(p.offsets + e + 1) - first : 0;
+      const int tiles = (rows + kTM - 1) / kTM;
+      int v = tiles;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
-          if (lane >= o) v += w;
-        }
-        if (e < p.E) pre[e + 1] = carry + v;
-        carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += w;
       }
+      if (e < p.E) ex[e] = {carry + v - tiles, first, rows, __ldg(p.sf_offsets + e)};
+      carry += __shfl_sync(0xFFFFFFFFu, v, 31);
     }
+    if (lane == 0) *all_tiles = carry;
   }
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();      // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int units = pre[p.E] * p.tiles_n;
+  const int units = *all_tiles * p.tiles_n;
 
   // a wait by the whole warp; false in all lanes if one gave up
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
@@ -315,7 +322,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
       uint32_t parity = 1;
       bool ok = true;
       for (int u = cta; ok && u < units; u += ctas) {
-        const Fp4Tile t = fp4_tile<PAIR>(p, pre, u, CH, rank);
+        const Fp4Tile t = fp4_tile<PAIR>(p, ex, u, CH, rank);
         const int wrow = static_cast<int>(t.e * p.N + t.n0);
         const int up = FUSED ? static_cast<int>(p.I) : 128;       // from the first 128 weight rows to the second
         const int pieces = (t.cnt + p.box - 1) / p.box;
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
         const bool two = FUSED || (BN == 256 && t.n0 + 128 < p.N);
         int pair_pieces = 0;                                      // of both CTAs, and which have token scales
         if constexpr (PAIR) {
-          const int other = rank ? 128 : max(0, fp4_tile<PAIR>(p, pre, u, CH, 1).cnt);
+          const int other = rank ? 128 : max(0, fp4_tile<PAIR>(p, ex, u, CH, 1).cnt);
           pair_pieces = pieces + (other + p.box - 1) / p.box;
         }
         for (int kb = 0; kb < p.kstages; ++kb) {
@@ -347,7 +354,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
               tma_load_2d_pair(s + C::SF_BYTES, &tmWS, bar, 0, static_cast<int>(wblk) * p.kb + y);
               tma_load_2d_pair(s + 2 * C::SF_BYTES, &tmWS, bar, 0, static_cast<int>(wblk + (up >> 7)) * p.kb + y);
               for (int i = 0; i < pieces; ++i)
-                tma_load_2d_pair(a + i * p.box * kStageBytes, &tmT, bar, x, static_cast<int>(t.t0) + i * p.box);
+                tma_load_2d_pair(a + i * p.box * kStageBytes, &tmT, bar, x, t.t0 + i * p.box);
               tma_load_2d_pair(s, &tmTS, bar, 0, static_cast<int>(t.tblk) * p.kb + y);
             } else {
               const uint32_t sfb = min(C::NKB, p.kb - kb * C::NKB) * 512;
@@ -358,7 +365,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
               bulk_load(s + C::SF_BYTES, sfw + sfo, sfb, &full[st]);
               if (two) bulk_load(s + 2 * C::SF_BYTES, sfw + second + sfo, sfb, &full[st]);
               for (int i = 0; i < pieces; ++i)
-                tma_load_2d(a + i * p.box * kStageBytes, &tmT, &full[st], x, static_cast<int>(t.t0) + i * p.box);
+                tma_load_2d(a + i * p.box * kStageBytes, &tmT, &full[st], x, t.t0 + i * p.box);
               bulk_load(s, sft + sfo, sfb, &full[st]);
             }
           }
@@ -390,7 +397,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
         for (int u = cta; ok && u < units; u += ctas) {
           // 64-column tiles: the second half of a 128-row scale block lies two columns on
           const uint32_t wcol =
-              C::SMALL ? static_cast<uint32_t>((fp4_tile<PAIR>(p, pre, u, CH, 0).n0 & 64) >> 5) : 0u;
+              C::SMALL ? static_cast<uint32_t>((fp4_tile<PAIR>(p, ex, u, CH, 0).n0 & 64) >> 5) : 0u;
           if (!warp_wait(&tempty[buf], acc_parity)) { ok = false; break; }
           tc_fence_after();
           for (int kb = 0; kb < p.kstages; ++kb) {
@@ -468,7 +475,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
     uint32_t parity = 0;
     bool ok = true;
     for (int u = cta; ok && u < units; u += ctas) {
-      const Fp4Tile t = fp4_tile<PAIR>(p, pre, u, CH, rank);
+      const Fp4Tile t = fp4_tile<PAIR>(p, ex, u, CH, rank);
       const float alpha = p.gb ? ga * p.gb[t.e] : ga;
       if constexpr (!FUSED) {
         if (!warp_wait(&tfull[buf], parity)) { ok = false; break; }
@@ -493,22 +500,37 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
         }
         give_back(buf);
         if (++buf == NB) { buf = 0; parity ^= 1u; }
-        if (r < t.cnt) {
-          const int64_t n = t.n0 + col0;
-          uint16_t* y = p.y + (t.t0 + r) * p.ldy + n;
-          if (p.vec32 && n + COLS <= p.N) {
+        const int64_t n = t.n0 + col0;
+        if constexpr (C::STAGED) {
+          // A lane's row of 64 columns (128 bytes) through shared memory, 16-byte
+          // chunks XORed by the row, so that eight lanes store a whole line of y:
+          // stored from the lane that holds it, a 32-byte piece costs a line's
+          // transaction (a 128 x 256 tile's stores took ~5000 cycles).
+          uint8_t* mine = sOut + (warp - 2) * 4096;
 #pragma unroll
-            for (int c = 0; c < COLS / 2; c += 8)
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + 2 * c),
-                           "r"(o[c]), "r"(o[c + 1]), "r"(o[c + 2]), "r"(o[c + 3]), "r"(o[c + 4]), "r"(o[c + 5]),
-                           "r"(o[c + 6]), "r"(o[c + 7])
-                           : "memory");
-          } else {
+          for (int c = 0; c < COLS / 2; c += 32) {
+            __syncwarp();
 #pragma unroll
-            for (int c = 0; c < COLS / 2; c += 4)
-              if (n + 2 * c < p.N)
-                *reinterpret_cast<uint4*>(y + 2 * c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(mine + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                  make_uint4(o[c + 4 * i], o[c + 4 * i + 1], o[c + 4 * i + 2], o[c + 4 * i + 3]);
+            __syncwarp();
+            const int64_t col = n + 2 * c + 8 * (lane & 7);
+            uint16_t* y = p.y + static_cast<int64_t>(t.t0 + quad * 32) * p.ldy + col;
+            if (col < p.N) {
+#pragma unroll
+              for (int i = lane >> 3; i < 32; i += 4)
+                if (quad * 32 + i < t.cnt)
+                  *reinterpret_cast<uint4*>(y + i * p.ldy) =
+                      *reinterpret_cast<const uint4*>(mine + i * 128 + (((lane ^ i) & 7) << 4));
+            }
           }
+        } else if (r < t.cnt) {
+          uint16_t* y = p.y + static_cast<int64_t>(t.t0 + r) * p.ldy + n;
+#pragma unroll
+          for (int c = 0; c < COLS / 2; c += 4)
+            if (n + 2 * c < p.N)
+              *reinterpret_cast<uint4*>(y + 2 * c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
         }
       } else {
         // The same gate and up columns of the thread's row; the accumulator
@@ -548,7 +570,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
 #pragma unroll
             for (int i = 0; i < G; i += 8) code[(j + i) / 8] = fp4_codes8<FMT>(y + i, s);
           }
-          uint4* q = reinterpret_cast<uint4*>(p.hq + (t.t0 + r) * (p.I >> 1) + (n >> 1));
+          uint4* q = reinterpret_cast<uint4*>(p.hq + static_cast<int64_t>(t.t0 + r) * (p.I >> 1) + (n >> 1));
 #pragma unroll
           for (int c = 0; c < COLS / 8; c += 4)
             q[c / 4] = make_uint4(code[c], code[c + 1], code[c + 2], code[c + 3]);
@@ -618,9 +640,9 @@ bool fp4_scale_map(const void* ptr, int64_t blocks, int rows, CUtensorMap* out) 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kStaticSmem = 4 * (kMaxExperts + 1) + 12;
-constexpr int kSmemMax = 227 * 1024 - kStaticSmem;
-constexpr int kSmemHalf = 113 * 1024 - kStaticSmem;   // two CTAs in 228 KB, 1 KB of each reserved
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kSmemHalf = 113 * 1024;   // two CTAs in 228 KB, 1 KB of each reserved
+constexpr int kBarBytes = 8 * 34;       // barriers, tensor memory address, abort flag, tile count
 
 template <int FMT, int CH, bool FUSED, bool PAIR>
 fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p, cudaStream_t stream) {
@@ -642,7 +664,7 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
   // the last stage's must stay inside the allocation.
   p.a_bytes = p.M <= 128 ? static_cast<int>((p.M + p.box - 1) / p.box) * p.box * kStageBytes : 128 * kStageBytes;
   const int stage = p.a_bytes + C::B_BYTES + C::SF_STAGE;
-  const int slack = 1024 + 256 + 128 * kStageBytes - p.a_bytes;   // alignment, barriers, that reach
+  const int slack = 1024 + C::OUT_BYTES + kBarBytes + 16 * p.E + 128 * kStageBytes - p.a_bytes;   // alignment, ..., that reach
   const int budget = C::SMALL ? kSmemHalf : kSmemMax;
   p.stages = (budget - slack) / stage;
   if (p.stages > 12) p.stages = 12;
@@ -680,17 +702,28 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
 template <int FMT, bool FUSED>
 fp8q_status run_fp4(const void* t, const void* w, Fp4Args& p, cudaStream_t stream) {
   // token tiles: at most this many (an expert's last one may be ragged)
-  const int64_t tt = p.offsets ? p.M / 128 + (p.M < p.E ? p.M : p.E) : (p.M + 127) / 128;
+  auto tiles = [&](int64_t tm) {
+    return p.offsets ? p.M / tm + (p.M < p.E ? p.M : p.E) : (p.M + tm - 1) / tm;
+  };
+  const int64_t tt = tiles(128);
   const int64_t per = p.offsets ? (p.M + p.E - 1) / p.E : p.M;      // rows of an expert, on average
   p.box = per > 64 ? 128 : p.M <= 16 ? 16 : 32;
   const int64_t nw = FUSED ? p.I : p.N, sms = num_sms();
+  static const int V = getenv("V") ? atoi(getenv("V")) : 0;
   if constexpr (FUSED) {
+    if (V == 1) return launch_fp4<FMT, 64, true, false>(t, w, tt, p, stream);
+    if (V == 2) return launch_fp4<FMT, 128, true, false>(t, w, tt, p, stream);
+    if (V == 3) return launch_fp4<FMT, 128, true, true>(t, w, tiles(256), p, stream);
     if (tt * (nw / 128) < sms) return launch_fp4<FMT, 64, true, false>(t, w, tt, p, stream);
     return launch_fp4<FMT, 128, true, false>(t, w, tt, p, stream);
   } else {
+    if (V == 1) return launch_fp4<FMT, 64, false, false>(t, w, tt, p, stream);
+    if (V == 2) return launch_fp4<FMT, 128, false, false>(t, w, tt, p, stream);
+    if (V == 3) return launch_fp4<FMT, 256, false, true>(t, w, tiles(256), p, stream);
+    if (V == 4) return launch_fp4<FMT, 256, false, false>(t, w, tt, p, stream);
     if (per <= 64 || tt * ((nw + 127) / 128) < sms) return launch_fp4<FMT, 64, false, false>(t, w, tt, p, stream);
-    if (!p.offsets && ((p.M + 255) / 256) * ((nw + 255) / 256) >= sms / 2)
-      return launch_fp4<FMT, 256, false, true>(t, w, (p.M + 255) / 256, p, stream);
+    if (!p.offsets && tiles(256) * ((nw + 255) / 256) >= sms / 2)
+      return launch_fp4<FMT, 256, false, true>(t, w, tiles(256), p, stream);
     if (tt * ((nw + 255) / 256) < sms) return launch_fp4<FMT, 128, false, false>(t, w, tt, p, stream);
     return launch_fp4<FMT, 256, false, false>(t, w, tt, p, stream);
   }
@@ -732,7 +765,6 @@ fp8q_status check_y(void* y, int64_t ldy, int64_t M, int64_t N, Fp4Args* p) {
   if (ldy < N || ldy % 8 != 0 || (M > 0 && (!y || !aligned(y, 16)))) return FP8Q_ERR_INVALID_ARG;
   p->y = static_cast<uint16_t*>(y);
   p->ldy = ldy;
-  p->vec32 = aligned(y, 32) && ldy % 16 == 0;
   return FP8Q_OK;
 }
 
