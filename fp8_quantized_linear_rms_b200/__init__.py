@@ -544,6 +544,11 @@ def _fp4(fmt: str):
         raise ValueError(f"format must be 'nvfp4' or 'mxfp4', got {fmt!r}") from None
 
 
+# the raw current stream of a device, without the Stream object of the public call (3 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _launch_stream(stream, first: torch.Tensor, *rest) -> int | None:
     """The raw stream to launch on; every tensor must be on the current device
     (the kernels, and the outputs allocated for them, go there)."""
@@ -553,7 +558,7 @@ def _launch_stream(stream, first: torch.Tensor, *rest) -> int | None:
             raise ValueError("all tensors must be on one device")
     if dev != torch.cuda.current_device():
         raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 def _torch_stream(stream):
@@ -564,7 +569,7 @@ def _empty(shape, dtype, like: torch.Tensor, stream):
     """A tensor that belongs to the stream the kernels run on, so that its
     memory is not handed on while they still use it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(_torch_stream(stream)):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -605,15 +610,18 @@ def fp4_sf_shape(rows: int, K: int, fmt: str):
 
 
 def _fp4_quant_out(M, K, group, x, q, sf, stream):
+    """Outputs, made here or the caller's (checked): q, its row stride, sf, its address."""
     if q is None:
-        q = _empty((M, K // 2), torch.uint8, x, stream)
+        q, ldq = _empty((M, K // 2), torch.uint8, x, stream), K // 2
     else:
         _need(q, torch.uint8, "q")
         if tuple(q.shape) != (M, K // 2):
             raise ValueError(f"q must be [{M}, {K // 2}]")
+        ldq = _rowmajor(q, "q")
     if sf is None:
         sf = _empty(_sf_shape(M, K, group), torch.uint8, x, stream)
-    return q, _rowmajor(q, "q"), sf, _need_sf(sf, M, K, group, "sf")
+        return q, ldq, sf, sf.data_ptr()
+    return q, ldq, sf, _need_sf(sf, M, K, group, "sf")
 
 
 def fp8q_fp4_quant(x: torch.Tensor, fmt: str, gscale=None, q=None, sf=None, stream=None):
@@ -676,20 +684,21 @@ def fp8q_fp4_dequant(q: torch.Tensor, sf: torch.Tensor, fmt: str, gscale=None, y
     M, K = q.shape[0], 2 * q.shape[1]
     sp = _need_sf(sf, M, K, group, "sf")
     g = _gscale(gscale, 1, "gscale")
-    y = _y_out(y, M, K, q, stream)
-    st = lib.fp8q_fp4_dequant(q.data_ptr(), ldq, sp, f, g, M, K, y.data_ptr(), _rowmajor(y, "y"),
-                              _launch_stream(stream, q, sf, gscale, y))
+    y, ldy = _y_out(y, M, K, q, stream)
+    st = lib.fp8q_fp4_dequant(q.data_ptr(), ldq, sp, f, g, M, K, y.data_ptr(), ldy,
+                                _launch_stream(stream, q, sf, gscale, y))
     _check("fp8q_fp4_dequant", st)
     return y
 
 
 def _y_out(y, M, N, like, stream):
+    """y, made here or the caller's (checked), and its row stride."""
     if y is None:
-        return _empty((M, N), torch.bfloat16, like, stream)
+        return _empty((M, N), torch.bfloat16, like, stream), N
     _need(y, torch.bfloat16, "y")
     if tuple(y.shape) != (M, N):
         raise ValueError(f"y must be [{M}, {N}]")
-    return y
+    return y, _rowmajor(y, "y")
 
 
 def fp8q_scaled_mm_fp4(a_q: torch.Tensor, b_q: torch.Tensor, a_sf: torch.Tensor, b_sf: torch.Tensor, fmt: str,
@@ -706,9 +715,8 @@ def fp8q_scaled_mm_fp4(a_q: torch.Tensor, b_q: torch.Tensor, a_sf: torch.Tensor,
     ap = _need_sf(a_sf, M, 2 * K2, group, "a_sf")
     bp = _need_sf(b_sf, N, 2 * K2, group, "b_sf")
     ga, gb = _gscale(a_gscale, 1, "a_gscale"), _gscale(b_gscale, 1, "b_gscale")
-    y = _y_out(y, M, N, a_q, stream)
-    st = lib.fp8q_scaled_mm_fp4(a_q.data_ptr(), b_q.data_ptr(), ap, bp, f, ga, gb, M, N, 2 * K2, y.data_ptr(),
-                                _rowmajor(y, "y"),
+    y, ldy = _y_out(y, M, N, a_q, stream)
+    st = lib.fp8q_scaled_mm_fp4(a_q.data_ptr(), b_q.data_ptr(), ap, bp, f, ga, gb, M, N, 2 * K2, y.data_ptr(), ldy,
                                 _launch_stream(stream, a_q, b_q, a_sf, b_sf, a_gscale, b_gscale, y))
     _check("fp8q_scaled_mm_fp4", st)
     return y
@@ -740,10 +748,12 @@ def fp8q_moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", b
         _gscale(bias, E, "bias")
     if weights is None:
         weights = _empty((T, top_k), torch.float32, logits, stream)
+    else:
+        _need_entries(weights, torch.float32, T, top_k, "weights")
     if ids is None:
         ids = _empty((T, top_k), torch.int32, logits, stream)
-    _need_entries(weights, torch.float32, T, top_k, "weights")
-    _need_entries(ids, torch.int32, T, top_k, "ids")
+    else:
+        _need_entries(ids, torch.int32, T, top_k, "ids")
     st = lib.fp8q_moe_route(logits.data_ptr(), logits.dtype is torch.bfloat16, T, E, ld if T > 1 else max(ld, E),
                             top_k, _SCORING[scoring], None if bias is None else bias.data_ptr(), num_groups,
                             topk_groups, bool(renormalize), scale, weights.data_ptr(), ids.data_ptr(),
@@ -833,10 +843,9 @@ def fp8q_grouped_mm_fp4(a_q: torch.Tensor, b_q: torch.Tensor, a_sf: torch.Tensor
     plan orders them), b_q [E, N, K/2] and b_sf [E, *fp4_sf_shape(N, K, fmt)]; a_gscale fp32 [1],
     b_gscale fp32 [E].  Rows without an expert are not written."""
     f, group, M, N, K, E, ga, gb = _grouped(a_q, b_q, a_sf, b_sf, fmt, plan, a_gscale, b_gscale)
-    y = _y_out(y, M, N, a_q, stream)
+    y, ldy = _y_out(y, M, N, a_q, stream)
     st = lib.fp8q_grouped_mm_fp4(a_q.data_ptr(), b_q.data_ptr(), a_sf.data_ptr(), b_sf.data_ptr(), f, ga, gb,
-                                 plan.offsets.data_ptr(), plan.sf_offsets.data_ptr(), E, M, N, K, y.data_ptr(),
-                                 _rowmajor(y, "y"),
+                                 plan.offsets.data_ptr(), plan.sf_offsets.data_ptr(), E, M, N, K, y.data_ptr(), ldy,
                                  _launch_stream(stream, a_q, b_q, a_sf, b_sf, a_gscale, b_gscale, y, *plan))
     _check("fp8q_grouped_mm_fp4", st)
     return y
@@ -869,9 +878,9 @@ def fp8q_moe_combine(o: torch.Tensor, plan: MoePlan, weights: torch.Tensor, y=No
     if o.shape[0] != T * k:
         raise ValueError(f"o must have {T * k} rows")
     H = o.shape[1]
-    y = _y_out(y, T, H, o, stream)
+    y, ldy = _y_out(y, T, H, o, stream)
     st = lib.fp8q_moe_combine(o.data_ptr(), _rowmajor(o, "o"), plan.pos.data_ptr(), weights.data_ptr(), T, k, H,
-                              y.data_ptr(), _rowmajor(y, "y"), _launch_stream(stream, o, weights, y, plan.pos))
+                              y.data_ptr(), ldy, _launch_stream(stream, o, weights, y, plan.pos))
     _check("fp8q_moe_combine", st)
     return y
 
@@ -904,7 +913,7 @@ def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
     s13, s2 = _need_sf(w13_sf, I2, H, group, "w13_sf", E), _need_sf(w2_sf, H, I, group, "w2_sf", E)
     gx, gh = _gscale(x_gscale, 1, "x_gscale"), _gscale(h_gscale, 1, "h_gscale")
     g13, g2 = _gscale(w13_gscale, E, "w13_gscale"), _gscale(w2_gscale, E, "w2_gscale")
-    y = _y_out(y, T, H, x, stream)
+    y, ldy = _y_out(y, T, H, x, stream)
     if workspace is None:
         n = lib.fp8q_moe_experts_fp4_workspace_bytes(T, k, E, H, I, f)
         workspace = _empty((n,), torch.uint8, x, stream)
@@ -912,7 +921,7 @@ def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
         _need(workspace, torch.uint8, "workspace")
     st = lib.fp8q_moe_experts_fp4(
         x.data_ptr(), T, ldx, ids.data_ptr(), weights.data_ptr(), k, E, H, I, f, w13.data_ptr(), s13, w2.data_ptr(),
-        s2, gx, g13, gh, g2, y.data_ptr(), _rowmajor(y, "y"), workspace.data_ptr(), workspace.numel(),
+        s2, gx, g13, gh, g2, y.data_ptr(), ldy, workspace.data_ptr(), workspace.numel(),
         _launch_stream(stream, x, ids, weights, w13, w13_sf, w2, w2_sf, x_gscale, w13_gscale, h_gscale, w2_gscale, y,
                        workspace))
     _check("fp8q_moe_experts_fp4", st)

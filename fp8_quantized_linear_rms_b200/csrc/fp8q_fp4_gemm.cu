@@ -16,10 +16,12 @@
 // Tokens sit in the MMA's 128 rows, weights in its BN columns, at every size.
 // A tile of few tokens copies only the 16- or 32-row pieces that hold some;
 // the MMA then computes rows that nobody reads, at no cost where the time is
-// that of reading the weights.  Few tokens take 64 weight rows a tile (the
-// narrowest that may begin inside a 128-row scale block: a 64-column MMA finds
-// its scales two tensor memory columns further), so that a layer spreads over
-// the SMs, two CTAs each; many take 256.
+// that of reading the weights.  Where 128-row tiles do not fill the SMs (few
+// tokens), a tile has 64 weight rows (the narrowest that may begin inside a
+// 128-row scale block: a 64-column MMA finds its scales two tensor memory
+// columns further), up to four CTAs share an SM, and a cluster of up to eight
+// CTAs splits the depth of one tile: each sums its part, and they add the
+// parts over distributed shared memory in a fixed order.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -58,8 +60,9 @@ struct Fp4Args {
   int64_t I;
   int tiles_n;                 // weight tiles of an expert
   int box;                     // token rows of one copy (16, 32, 128)
-  int stages;
+  int stages, ring;            // stages of the ring, and its bytes (a split tile's part lies there too)
   int a_bytes;                 // shared memory of a stage's token tile
+  int split;                   // CTAs that share a tile's depth (64-row tiles; 1: none)
   int* status;
 };
 
@@ -183,7 +186,8 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const Fp4Expert* e
 // CH output columns a tile: 64, 128 or 256 weight rows, or FUSED 64 or 128
 // hidden channels, whose gate rows are followed by the up rows.  128 channels
 // are one 256-column MMA, 64 are two 64-column ones (gate, up), each with the
-// scale block that its rows lie in.  PAIR: two CTAs of a cluster share one MMA
+// scale block that its rows lie in.  64 rows or channels: SMALL, one tile a
+// cluster.  PAIR: two CTAs of a cluster share one MMA
 // of 256 token rows and 256 columns (tcgen05 cta_group::2), each with 128 of
 // the rows of both operands in its shared memory, so a weight row reaches each
 // SM half as often; each holds the scales of its own tokens and of all columns.
@@ -192,7 +196,8 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const Fp4Expert* e
 // more than the 256-column one: 1341 against 894 us at 8192 x 51200 x 5120).
 template <int FMT, int CH, bool FUSED, bool PAIR>
 struct Fp4Cfg {
-  static constexpr bool SMALL = CH == 64;                   // two CTAs on an SM
+  static constexpr bool SMALL = CH == 64;
+  static constexpr int PER_SM = SMALL ? (FUSED ? 2 : 4) : 1;        // CTAs on an SM, by tensor memory
   static constexpr int BN = FUSED ? 2 * CH : CH;            // accumulator columns
   static constexpr bool TWO_MMA = FUSED && SMALL;
   static constexpr int MMA_N = TWO_MMA ? CH : BN;
@@ -206,22 +211,23 @@ struct Fp4Cfg {
   static constexpr int B_BYTES = (PAIR ? 128 : BN) * kStageBytes;
   static constexpr int SF_STAGE = (1 + BBLK) * SF_BYTES;
   static constexpr int SF_TMEM = (1 + BBLK) * SF_COLS;      // tensor memory columns of a stage's scales
-  static constexpr int SFBUF = SMALL ? 2 : 4;
-  static constexpr int NBUF = BN == 256 || TWO_MMA ? 1 : 2; // accumulators
+  static constexpr int SFBUF = SMALL ? 1 : 4;               // stages' scales in tensor memory at once
+  static constexpr int NBUF = BN == 256 || SMALL ? 1 : 2;   // accumulators
   static constexpr int ACC_COLS = NBUF * BN;
-  static constexpr int TMEM = SMALL ? 256 : 512;
+  static constexpr int TMEM = 512 / PER_SM;
   static constexpr bool STAGED = !FUSED && !SMALL;          // y leaves through shared memory
   static constexpr int OUT_BYTES = STAGED ? EPI_WARPS * 4096 : 0;
   // tensor memory columns of the weight scales: from one K block to the next, and between their
   // 128-row blocks (side by side for one 256-column MMA)
   static constexpr int B_STEP = MMA_N == 256 ? 8 : 4;
   static constexpr int B_BLOCK = MMA_N == 256 ? 4 : SF_COLS;
-  static_assert(ACC_COLS + SFBUF * SF_TMEM + 4 <= TMEM, "tensor memory");
+  // a 64-column MMA of the upper half of a block reads two columns further
+  static_assert(ACC_COLS + SFBUF * SF_TMEM + 2 <= TMEM, "tensor memory");
   static_assert(!PAIR || BN == 256, "pairs have 256 columns");
 };
 
 template <int FMT, int CH, bool FUSED, bool PAIR>
-__global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<FMT, CH, FUSED, PAIR>::SMALL ? 2 : 1)
+__global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<FMT, CH, FUSED, PAIR>::PER_SM)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmTS, const __grid_constant__ CUtensorMap tmWS,
                     const Fp4Args p) {
@@ -234,7 +240,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
   uint8_t* sA = smem;
   uint8_t* sB = sA + S * p.a_bytes;
   uint8_t* sSF = sB + S * C::B_BYTES;
-  uint8_t* sOut = sSF + S * C::SF_STAGE;
+  uint8_t* sOut = smem + p.ring;
   uint64_t* full = reinterpret_cast<uint64_t*>(sOut + C::OUT_BYTES);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
@@ -247,8 +253,13 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-  const int cta = PAIR ? static_cast<int>(blockIdx.x >> 1) : static_cast<int>(blockIdx.x);    // of the tile loop
-  const int ctas = PAIR ? static_cast<int>(gridDim.x >> 1) : static_cast<int>(gridDim.x);
+  // the tile loop: first tile and step; SMALL: one tile, of whose depth this
+  // CTA takes stages [k0, k1)
+  const int group = C::SMALL ? p.split : PAIR ? 2 : 1;
+  const int cta = static_cast<int>(blockIdx.x) / group, ctas = static_cast<int>(gridDim.x) / group;
+  const int part = C::SMALL ? static_cast<int>(blockIdx.x) - cta * group : 0;
+  const int k0 = C::SMALL ? p.kstages * part / p.split : 0;
+  const int k1 = C::SMALL ? p.kstages * (part + 1) / p.split : p.kstages;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -277,7 +288,6 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
     }
   }
   griddep_wait();
-  griddep_launch_dependents();
 
   constexpr int kTM = PAIR ? 256 : 128;
   if (p.offsets == nullptr) {
@@ -285,26 +295,32 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
       ex[0] = {0, 0, static_cast<int>(p.M), 0};
       *all_tiles = static_cast<int>((p.M + kTM - 1) / kTM);
     }
-  } else if (warp == 0) {
-    int carry = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int first = e < p.E ? __ldg(p.offsets + e) : 0;
-      const int rows = e < p.E ? __ldg(p.offsets + e + 1) - first : 0;
-      const int tiles = (rows + kTM - 1) / kTM;
-      int v = tiles;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if (lane >= o) v += w;
-      }
-      if (e < p.E) ex[e] = {carry + v - tiles, first, rows, __ldg(p.sf_offsets + e)};
-      carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+  } else {
+    for (int e = threadIdx.x; e < p.E; e += C::THREADS) {
+      const int first = __ldg(p.offsets + e), end = __ldg(p.offsets + e + 1);
+      ex[e] = {0, first, end - first, __ldg(p.sf_offsets + e)};
     }
-    if (lane == 0) *all_tiles = carry;
+    __syncthreads();
+    if (warp == 0) {
+      int carry = 0;
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int tiles = e < p.E ? (ex[e].rows + kTM - 1) / kTM : 0;
+        int v = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int w = __shfl_up_sync(0xFFFFFFFFu, v, o);
+          if (lane >= o) v += w;
+        }
+        if (e < p.E) ex[e].tiles = carry + v - tiles;
+        carry += __shfl_sync(0xFFFFFFFFu, v, 31);
+      }
+      if (lane == 0) *all_tiles = carry;
+    }
   }
   tc_fence_before();
   __syncthreads();
+  griddep_launch_dependents();             // this CTA has its tensor memory: a dependent cannot take it first
   if constexpr (PAIR) cluster_sync();      // both CTAs' barriers are ready
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -337,7 +353,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
           const int other = rank ? 128 : max(0, fp4_tile<PAIR>(p, ex, u, CH, 1).cnt);
           pair_pieces = pieces + (other + p.box - 1) / p.box;
         }
-        for (int kb = 0; kb < p.kstages; ++kb) {
+        for (int kb = k0; kb < k1; ++kb) {
           if (!warp_wait(&empty[st], parity)) { ok = false; break; }
           uint8_t* a = sA + st * p.a_bytes;
           uint8_t* b = sB + st * C::B_BYTES;
@@ -400,7 +416,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
               C::SMALL ? static_cast<uint32_t>((fp4_tile<PAIR>(p, ex, u, CH, 0).n0 & 64) >> 5) : 0u;
           if (!warp_wait(&tempty[buf], acc_parity)) { ok = false; break; }
           tc_fence_after();
-          for (int kb = 0; kb < p.kstages; ++kb) {
+          for (int kb = k0; kb < k1; ++kb) {
             if (!warp_wait(&full[st], parity)) { ok = false; break; }
             tc_fence_after();
             const uint32_t sfa = tmem + C::ACC_COLS + sbuf * C::SF_TMEM;
@@ -418,7 +434,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
                   // nvfp4: a K slice has a scale block of its own; mxfp4: two share one, ids 0 and 2
                   const int b = FMT == kNv ? k : k >> 1;
                   const uint32_t id = FMT == kNv ? 0u : 2u * (k & 1);
-                  mma_fp4<FMT, PAIR>(d, ad + 2 * k, w + 2 * k, id0 | (id << 4) | (id << 29), kb > 0 || k > 0,
+                  mma_fp4<FMT, PAIR>(d, ad + 2 * k, w + 2 * k, id0 | (id << 4) | (id << 29), kb > k0 || k > 0,
                                      (sfa + b * 4) | (id << 30), (sw + b * C::B_STEP) | (id << 30));
                 }
               }
@@ -438,7 +454,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
               mmas(d, bd, sfb);
               if constexpr (C::TWO_MMA) mmas(d + CH, bd + (CH * kStageBytes >> 4), sfb + C::B_BLOCK);
               commit(&empty[st]);
-              if (kb + 1 == p.kstages) commit(&tfull[buf]);
+              if (kb + 1 == k1) commit(&tfull[buf]);
             }
             __syncwarp();
             if (++st == S) { st = 0; parity ^= 1u; }
@@ -471,6 +487,16 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
         else mbar_arrive(&tempty[buf]);
       }
     };
+    // 32 columns of this CTA's part of a split tile, fp32, over the ring (whose
+    // copies and MMAs are done): row r at r BN, 16-byte chunks XORed by the row
+    auto keep_part = [&](uint32_t acc, int col, int row) {
+      uint32_t v[32];
+      tmem_ld_waited<32>(acc, v);
+      uint4* d = reinterpret_cast<uint4*>(smem + row * (BN * 4));
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        d[(col / 4 + i) ^ (row & 7)] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    };
     int buf = 0;
     uint32_t parity = 0;
     bool ok = true;
@@ -480,6 +506,13 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
       if constexpr (!FUSED) {
         if (!warp_wait(&tfull[buf], parity)) { ok = false; break; }
         tc_fence_after();
+        if (C::SMALL && p.split > 1) {
+          if (quad * 32 < t.cnt) {
+#pragma unroll
+            for (int c = 0; c < COLS; c += 32) keep_part(tmem + lane_addr + col0 + c, col0 + c, r);
+          }
+          continue;
+        }
         // The thread's columns, rounded to bf16 as they are read (the next 32 in
         // flight meanwhile), so that the accumulator goes back to the MMAs
         // before anything is stored.
@@ -540,6 +573,13 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
         tc_fence_after();
         const uint32_t acc = tmem + lane_addr + col0;
         const int64_t n = t.n0 + col0;
+        if (C::SMALL && p.split > 1) {
+          if (quad * 32 < t.cnt) {
+            keep_part(acc, col0, r);
+            keep_part(acc + CH, CH + col0, r);
+          }
+          continue;
+        }
         uint32_t g[COLS], w[COLS];
         if (quad * 32 < t.cnt) {
 #pragma unroll
@@ -584,6 +624,55 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
     }
   }
 
+  if constexpr (C::SMALL) {
+    if (p.split > 1) {
+      // The cluster's parts, added in the order of the depth; its CTAs take
+      // turns at groups of G neighbouring outputs of a row.
+      cluster_sync();
+      if (cta < units && *abort_flag == 0) {
+        constexpr int G = FUSED ? fp4_group<FMT>() : 8;
+        const Fp4Tile t = fp4_tile<PAIR>(p, ex, cta, CH, 0);
+        const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? p.gb[t.e] : 1.0f);
+        for (int i = part * C::THREADS + threadIdx.x; i < t.cnt * (CH / G); i += p.split * C::THREADS) {
+          const int row = i / (CH / G), col = (i - row * (CH / G)) * G;
+          float v[FUSED ? 2 * G : G] = {};
+          for (int q = 0; q < p.split; ++q) {
+            const uint32_t src = mapa_shared(smem_u32(smem), q) + row * (BN * 4);
+#pragma unroll
+            for (int j = 0; j < (FUSED ? 2 * G : G); j += 4) {
+              const int c = j < G ? col + j : CH + col + j - G;
+              float f[4];
+              asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+                           : "r"(src + (((c / 4) ^ (row & 7)) << 4))
+                           : "memory");
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[j + k] += f[k];
+            }
+          }
+          const int64_t n = t.n0 + col;
+          if constexpr (FUSED) {
+            float y[G], amax = 0.0f;
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+              y[j] = silu_mul_f32(v[j] * alpha, v[G + j] * alpha);
+              amax = fmaxf(amax, fabsf(y[j]));
+            }
+            const Fp4Scale sc = fp4_scale<FMT>(amax, p.gh ? *p.gh : 1.0f);
+            uint32_t* q = reinterpret_cast<uint32_t*>(p.hq + static_cast<int64_t>(t.t0 + row) * (p.I >> 1) + (n >> 1));
+#pragma unroll
+            for (int j = 0; j < G; j += 8) q[j / 8] = fp4_codes8<FMT>(y + j, sc);
+            p.hsf[fp4_sf_offset(t.tblk * 128 + row, n / G, fp4_kblocks(FMT, p.I))] = static_cast<uint8_t>(sc.byte);
+          } else if (n < p.N) {
+            *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(t.t0 + row) * p.ldy + n) =
+                make_uint4(pack_bf16(v[0] * alpha, v[1] * alpha), pack_bf16(v[2] * alpha, v[3] * alpha),
+                           pack_bf16(v[4] * alpha, v[5] * alpha), pack_bf16(v[6] * alpha, v[7] * alpha));
+          }
+        }
+      }
+      cluster_sync();                        // no part is given up while another CTA reads it
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if constexpr (PAIR) cluster_sync();      // neither leaves while the other may use its memory
@@ -641,7 +730,7 @@ bool fp4_scale_map(const void* ptr, int64_t blocks, int rows, CUtensorMap* out) 
 }
 
 constexpr int kSmemMax = 227 * 1024;
-constexpr int kSmemHalf = 113 * 1024;   // two CTAs in 228 KB, 1 KB of each reserved
+constexpr int kSmemSm = 228 * 1024;     // of an SM; 1 KB of each CTA's share is reserved
 constexpr int kBarBytes = 8 * 34;       // barriers, tensor memory address, abort flag, tile count
 
 template <int FMT, int CH, bool FUSED, bool PAIR>
@@ -660,24 +749,43 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
   }
   p.tiles_n = static_cast<int>(((FUSED ? p.I : p.N) + CH - 1) / CH);
   // A tile that is known to have fewer rows keeps less of them; its MMA reads
-  // 128 rows' worth of shared memory from the tile's start all the same, so
-  // the last stage's must stay inside the allocation.
+  // 128 rows' worth of shared memory from the tile's start all the same.
   p.a_bytes = p.M <= 128 ? static_cast<int>((p.M + p.box - 1) / p.box) * p.box * kStageBytes : 128 * kStageBytes;
   const int stage = p.a_bytes + C::B_BYTES + C::SF_STAGE;
-  const int slack = 1024 + C::OUT_BYTES + kBarBytes + 16 * p.E + 128 * kStageBytes - p.a_bytes;   // alignment, ..., that reach
-  const int budget = C::SMALL ? kSmemHalf : kSmemMax;
-  p.stages = (budget - slack) / stage;
-  if (p.stages > 12) p.stages = 12;
-  const int smem = p.stages * stage + slack;
+  const int fixed = 1024 + C::OUT_BYTES + kBarBytes + 16 * p.E;      // alignment, ...
+  const int64_t units = tiles_t * p.tiles_n;
+  auto stages = [&](int per_sm) {
+    const int n = ((per_sm == 1 ? kSmemMax : kSmemSm / per_sm - 1024) - fixed) / stage;
+    return n > 12 ? 12 : n;
+  };
+  int per_sm = 1, part = 0;
+  p.split = 1;
+  if (C::SMALL) {
+    while (p.split < 8 && 2 * p.split * units <= C::PER_SM * num_sms() && 4 * p.split <= p.kstages) p.split *= 2;
+    // as many CTAs on an SM as the grid has use for, each with a ring of four stages at least
+    while (per_sm < C::PER_SM && per_sm * num_sms() < units * p.split && stages(per_sm + 1) >= 4) ++per_sm;
+    if (p.split > 1) part = (p.M < 128 ? static_cast<int>(p.M + 31) / 32 * 32 : 128) * C::BN * 4;
+  }
+  p.stages = stages(per_sm);
+  p.ring = p.stages * stage;
+  // the MMA's reach from the last stage's token tile, and a split tile's part
+  const int reach = (p.stages - 1) * p.a_bytes + 128 * kStageBytes;
+  if (p.ring < reach) p.ring = reach;
+  if (p.ring < part) p.ring = part;
+  int smem = fixed + p.ring;
+  // No less shared memory than the CTA's share of tensor memory: CTAs that fit
+  // an SM together then never wait for each other's tensor memory, which CTAs
+  // of a cluster that wait for one another must not do.
+  if (C::SMALL && smem < kSmemSm / C::PER_SM - 1024) smem = kSmemSm / C::PER_SM - 1024;
   auto kern = fp4_gemm_kernel<FMT, CH, FUSED, PAIR>;
-  static std::atomic<int> attr_done[64];     // pairs: clusters that fit the device
+  static std::atomic<int> attr_done[64];     // CTAs (pairs) that fit the device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8Q_ERR_CUDA;
   int fit = attr_done[dev].load(std::memory_order_relaxed);
   if (!fit) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, budget) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) != cudaSuccess)
       return FP8Q_ERR_CUDA;
-    fit = num_sms() * (C::SMALL ? 2 : 1);
+    fit = num_sms();
     if (PAIR) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
@@ -693,7 +801,9 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
     }
     attr_done[dev].store(fit, std::memory_order_relaxed);
   }
-  const int64_t units = tiles_t * p.tiles_n;
+  if (C::SMALL)
+    return launch_kernel(kern, dim3(static_cast<unsigned>(units * p.split)), dim3(C::THREADS), smem, stream, p.split,
+                         mt, mw, mts, mws, p);
   const unsigned grid = static_cast<unsigned>(units < fit ? units : fit) * (PAIR ? 2 : 1);
   return launch_kernel(kern, dim3(grid), dim3(C::THREADS), smem, stream, PAIR ? 2 : 1, mt, mw, mts, mws, p);
 }
@@ -721,7 +831,7 @@ fp8q_status run_fp4(const void* t, const void* w, Fp4Args& p, cudaStream_t strea
     if (V == 2) return launch_fp4<FMT, 128, false, false>(t, w, tt, p, stream);
     if (V == 3) return launch_fp4<FMT, 256, false, true>(t, w, tiles(256), p, stream);
     if (V == 4) return launch_fp4<FMT, 256, false, false>(t, w, tt, p, stream);
-    if (per <= 64 || tt * ((nw + 127) / 128) < sms) return launch_fp4<FMT, 64, false, false>(t, w, tt, p, stream);
+    if (tt * ((nw + 127) / 128) < sms || (per <= 64 && !p.offsets && V == 0)) return launch_fp4<FMT, 64, false, false>(t, w, tt, p, stream);
     if (!p.offsets && tiles(256) * ((nw + 255) / 256) >= sms / 2)
       return launch_fp4<FMT, 256, false, true>(t, w, tiles(256), p, stream);
     if (tt * ((nw + 255) / 256) < sms) return launch_fp4<FMT, 128, false, false>(t, w, tt, p, stream);
