@@ -17,11 +17,10 @@
 // A tile of few tokens copies only the 16- or 32-row pieces that hold some;
 // the MMA then computes rows that nobody reads, at no cost where the time is
 // that of reading the weights.  Where 128-row tiles do not fill the SMs (few
-// tokens), a tile has 64 weight rows (the narrowest that may begin inside a
-// 128-row scale block: a 64-column MMA finds its scales two tensor memory
-// columns further), up to four CTAs share an SM, and a cluster of up to eight
-// CTAs splits the depth of one tile: each sums its part, and they add the
-// parts over distributed shared memory in a fixed order.
+// tokens), a cluster of up to eight CTAs, two to an SM, splits the depth of a
+// tile: each sums its part, and they add the parts over distributed shared
+// memory in a fixed order.  (Narrower tiles instead: a 64-column MMA takes 59
+// cycles, a 128-column one 65, so a stage of half the weights took as long.)
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -62,7 +61,7 @@ struct Fp4Args {
   int box;                     // token rows of one copy (16, 32, 128)
   int stages, ring;            // stages of the ring, and its bytes (a split tile's part lies there too)
   int a_bytes;                 // shared memory of a stage's token tile
-  int split;                   // CTAs that share a tile's depth (64-row tiles; 1: none)
+  int split;                   // CTAs that share a tile's depth
   int* status;
 };
 
@@ -183,25 +182,25 @@ __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const Fp4Expert* e
 }
 
 // ------------------------------------------------------------------- kernel
-// CH output columns a tile: 64, 128 or 256 weight rows, or FUSED 64 or 128
-// hidden channels, whose gate rows are followed by the up rows.  128 channels
-// are one 256-column MMA, 64 are two 64-column ones (gate, up), each with the
-// scale block that its rows lie in.  64 rows or channels: SMALL, one tile a
-// cluster.  PAIR: two CTAs of a cluster share one MMA
+// CH output columns a tile: 128 or 256 weight rows, or FUSED 64 or 128 hidden
+// channels, whose gate rows are followed by the up rows.  128 channels are one
+// 256-column MMA, 64 are two 64-column ones (gate, up), each with the scale
+// block that its rows lie in; a tile that begins in the middle of a block finds
+// its scales two tensor memory columns further.  SPLIT: one tile a cluster,
+// whose CTAs share its depth.  PAIR: two CTAs of a cluster share one MMA
 // of 256 token rows and 256 columns (tcgen05 cta_group::2), each with 128 of
 // the rows of both operands in its shared memory, so a weight row reaches each
 // SM half as often; each holds the scales of its own tokens and of all columns.
 // Tried and slower: a tile as two 128-column MMAs and accumulators, so that one
 // is read while the other computes (a pair's 128-column MMA took ~140 cycles,
 // more than the 256-column one: 1341 against 894 us at 8192 x 51200 x 5120).
-template <int FMT, int CH, bool FUSED, bool PAIR>
+template <int FMT, int CH, bool FUSED, bool PAIR, bool SPLIT>
 struct Fp4Cfg {
-  static constexpr bool SMALL = CH == 64;
-  static constexpr int PER_SM = SMALL ? (FUSED ? 2 : 4) : 1;        // CTAs on an SM, by tensor memory
+  static constexpr int PER_SM = SPLIT ? 2 : 1;              // CTAs on an SM, by tensor memory
   static constexpr int BN = FUSED ? 2 * CH : CH;            // accumulator columns
-  static constexpr bool TWO_MMA = FUSED && SMALL;
+  static constexpr bool TWO_MMA = FUSED && CH == 64;
   static constexpr int MMA_N = TWO_MMA ? CH : BN;
-  static constexpr int EPI_WARPS = SMALL && !FUSED ? 4 : 8;
+  static constexpr int EPI_WARPS = SPLIT && !FUSED ? 4 : 8;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int NKB = FMT == kNv ? 4 : 2;            // scale blocks of a stage, per 128 rows
   static constexpr int SF_BYTES = NKB * 512;                // per 128 rows
@@ -211,11 +210,11 @@ struct Fp4Cfg {
   static constexpr int B_BYTES = (PAIR ? 128 : BN) * kStageBytes;
   static constexpr int SF_STAGE = (1 + BBLK) * SF_BYTES;
   static constexpr int SF_TMEM = (1 + BBLK) * SF_COLS;      // tensor memory columns of a stage's scales
-  static constexpr int SFBUF = SMALL ? 1 : 4;               // stages' scales in tensor memory at once
-  static constexpr int NBUF = BN == 256 || SMALL ? 1 : 2;   // accumulators
+  static constexpr int SFBUF = SPLIT ? 1 : 4;               // stages' scales in tensor memory at once
+  static constexpr int NBUF = BN == 256 || SPLIT ? 1 : 2;   // accumulators
   static constexpr int ACC_COLS = NBUF * BN;
   static constexpr int TMEM = 512 / PER_SM;
-  static constexpr bool STAGED = !FUSED && !SMALL;          // y leaves through shared memory
+  static constexpr bool STAGED = !FUSED && !SPLIT;          // y leaves through shared memory
   static constexpr int OUT_BYTES = STAGED ? EPI_WARPS * 4096 : 0;
   // tensor memory columns of the weight scales: from one K block to the next, and between their
   // 128-row blocks (side by side for one 256-column MMA)
@@ -223,15 +222,16 @@ struct Fp4Cfg {
   static constexpr int B_BLOCK = MMA_N == 256 ? 4 : SF_COLS;
   // a 64-column MMA of the upper half of a block reads two columns further
   static_assert(ACC_COLS + SFBUF * SF_TMEM + 2 <= TMEM, "tensor memory");
-  static_assert(!PAIR || BN == 256, "pairs have 256 columns");
+  static_assert(!PAIR || (BN == 256 && !SPLIT), "pairs have 256 columns");
+  static_assert(CH >= 128 || (FUSED && SPLIT), "64 channels: split tiles");
 };
 
-template <int FMT, int CH, bool FUSED, bool PAIR>
-__global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<FMT, CH, FUSED, PAIR>::PER_SM)
+template <int FMT, int CH, bool FUSED, bool PAIR, bool SPLIT>
+__global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::PER_SM)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmTS, const __grid_constant__ CUtensorMap tmWS,
                     const Fp4Args p) {
-  using C = Fp4Cfg<FMT, CH, FUSED, PAIR>;
+  using C = Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>;
   constexpr int BN = C::BN, NB = C::NBUF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -253,13 +253,13 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
-  // the tile loop: first tile and step; SMALL: one tile, of whose depth this
+  // the tile loop: first tile and step; SPLIT: one tile, of whose depth this
   // CTA takes stages [k0, k1)
-  const int group = C::SMALL ? p.split : PAIR ? 2 : 1;
+  const int group = SPLIT ? p.split : PAIR ? 2 : 1;
   const int cta = static_cast<int>(blockIdx.x) / group, ctas = static_cast<int>(gridDim.x) / group;
-  const int part = C::SMALL ? static_cast<int>(blockIdx.x) - cta * group : 0;
-  const int k0 = C::SMALL ? p.kstages * part / p.split : 0;
-  const int k1 = C::SMALL ? p.kstages * (part + 1) / p.split : p.kstages;
+  const int part = SPLIT ? static_cast<int>(blockIdx.x) - cta * group : 0;
+  const int k0 = SPLIT ? p.kstages * part / p.split : 0;
+  const int k1 = SPLIT ? p.kstages * (part + 1) / p.split : p.kstages;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -286,6 +286,19 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
       tmem_alloc(tmem_slot, C::TMEM);
       tmem_relinquish();
     }
+  }
+  if (warp == 0 && p.offsets == nullptr && cta < (p.M + 127) / 128 * p.tiles_n) {
+    // The first stages' weights into L2 while the previous kernel of the stream
+    // finishes: a hint (they are loaded again after the wait).
+    const int64_t tm = (p.M + (PAIR ? 255 : 127)) / (PAIR ? 256 : 128);
+    const int n0 = static_cast<int>(cta / tm) * CH + (PAIR ? rank * 128 : 0);
+    if (elect_one()) {
+      for (int kb = k0; kb < k1 && kb < k0 + S; ++kb) {
+        tma_prefetch_2d(&tmW, kb * kStageBytes, n0);
+        if (C::BBLK == 2 && !PAIR) tma_prefetch_2d(&tmW, kb * kStageBytes, n0 + 128);
+      }
+    }
+    __syncwarp();
   }
   griddep_wait();
 
@@ -413,7 +426,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
         for (int u = cta; ok && u < units; u += ctas) {
           // 64-column tiles: the second half of a 128-row scale block lies two columns on
           const uint32_t wcol =
-              C::SMALL ? static_cast<uint32_t>((fp4_tile<PAIR>(p, ex, u, CH, 0).n0 & 64) >> 5) : 0u;
+              CH == 64 ? static_cast<uint32_t>((fp4_tile<PAIR>(p, ex, u, CH, 0).n0 & 64) >> 5) : 0u;
           if (!warp_wait(&tempty[buf], acc_parity)) { ok = false; break; }
           tc_fence_after();
           for (int kb = k0; kb < k1; ++kb) {
@@ -506,7 +519,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
       if constexpr (!FUSED) {
         if (!warp_wait(&tfull[buf], parity)) { ok = false; break; }
         tc_fence_after();
-        if (C::SMALL && p.split > 1) {
+        if (SPLIT && p.split > 1) {
           if (quad * 32 < t.cnt) {
 #pragma unroll
             for (int c = 0; c < COLS; c += 32) keep_part(tmem + lane_addr + col0 + c, col0 + c, r);
@@ -573,7 +586,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
         tc_fence_after();
         const uint32_t acc = tmem + lane_addr + col0;
         const int64_t n = t.n0 + col0;
-        if (C::SMALL && p.split > 1) {
+        if (SPLIT && p.split > 1) {
           if (quad * 32 < t.cnt) {
             keep_part(acc, col0, r);
             keep_part(acc + CH, CH + col0, r);
@@ -624,7 +637,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR>::THREADS, Fp4Cfg<
     }
   }
 
-  if constexpr (C::SMALL) {
+  if constexpr (SPLIT) {
     if (p.split > 1) {
       // The cluster's parts, added in the order of the depth; its CTAs take
       // turns at groups of G neighbouring outputs of a row.
@@ -733,9 +746,9 @@ constexpr int kSmemMax = 227 * 1024;
 constexpr int kSmemSm = 228 * 1024;     // of an SM; 1 KB of each CTA's share is reserved
 constexpr int kBarBytes = 8 * 34;       // barriers, tensor memory address, abort flag, tile count
 
-template <int FMT, int CH, bool FUSED, bool PAIR>
+template <int FMT, int CH, bool FUSED, bool PAIR, bool SPLIT>
 fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p, cudaStream_t stream) {
-  using C = Fp4Cfg<FMT, CH, FUSED, PAIR>;
+  using C = Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>;
   CUtensorMap mt, mw, mts, mws;
   if (!fp4_tensor_map(t, p.M, p.K, p.box, &mt) || !fp4_tensor_map(w, p.E * p.N, p.K, C::BBOX, &mw))
     return FP8Q_ERR_CUDA;
@@ -760,10 +773,17 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
   };
   int per_sm = 1, part = 0;
   p.split = 1;
-  if (C::SMALL) {
-    while (p.split < 8 && 2 * p.split * units <= C::PER_SM * num_sms() && 4 * p.split <= p.kstages) p.split *= 2;
-    // as many CTAs on an SM as the grid has use for, each with a ring of four stages at least
-    while (per_sm < C::PER_SM && per_sm * num_sms() < units * p.split && stages(per_sm + 1) >= 4) ++per_sm;
+  if (SPLIT) {
+    // about one CTA an SM: a tile's depth in up to eight parts of two stages at
+    // least.  (More and shorter parts were slower: 1 x 5120 x 25600 nvfp4 took
+    // 18.1 us in 3 parts, 19.2 in 4; clusters that do not fit at once wait for
+    // the first to end, so split tiles leave room for two CTAs on an SM.)
+    p.split = static_cast<int>(units > 0 ? num_sms() / units : 1);
+    if (p.split > 8) p.split = 8;
+    if (p.split > p.kstages / 2) p.split = p.kstages / 2;
+    if (p.split < 1) p.split = 1;
+    { const char* e = getenv("SPL"); if (e && atoi(e)) p.split = atoi(e); }
+    if (units * p.split > num_sms() || p.split > 1) per_sm = 2;
     if (p.split > 1) part = (p.M < 128 ? static_cast<int>(p.M + 31) / 32 * 32 : 128) * C::BN * 4;
   }
   p.stages = stages(per_sm);
@@ -776,8 +796,8 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
   // No less shared memory than the CTA's share of tensor memory: CTAs that fit
   // an SM together then never wait for each other's tensor memory, which CTAs
   // of a cluster that wait for one another must not do.
-  if (C::SMALL && smem < kSmemSm / C::PER_SM - 1024) smem = kSmemSm / C::PER_SM - 1024;
-  auto kern = fp4_gemm_kernel<FMT, CH, FUSED, PAIR>;
+  if (SPLIT && smem < kSmemSm / C::PER_SM - 1024) smem = kSmemSm / C::PER_SM - 1024;
+  auto kern = fp4_gemm_kernel<FMT, CH, FUSED, PAIR, SPLIT>;
   static std::atomic<int> attr_done[64];     // CTAs (pairs) that fit the device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8Q_ERR_CUDA;
@@ -801,7 +821,7 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
     }
     attr_done[dev].store(fit, std::memory_order_relaxed);
   }
-  if (C::SMALL)
+  if (SPLIT)
     return launch_kernel(kern, dim3(static_cast<unsigned>(units * p.split)), dim3(C::THREADS), smem, stream, p.split,
                          mt, mw, mts, mws, p);
   const unsigned grid = static_cast<unsigned>(units < fit ? units : fit) * (PAIR ? 2 : 1);
@@ -821,21 +841,22 @@ fp8q_status run_fp4(const void* t, const void* w, Fp4Args& p, cudaStream_t strea
   const int64_t nw = FUSED ? p.I : p.N, sms = num_sms();
   static const int V = getenv("V") ? atoi(getenv("V")) : 0;
   if constexpr (FUSED) {
-    if (V == 1) return launch_fp4<FMT, 64, true, false>(t, w, tt, p, stream);
-    if (V == 2) return launch_fp4<FMT, 128, true, false>(t, w, tt, p, stream);
-    if (V == 3) return launch_fp4<FMT, 128, true, true>(t, w, tiles(256), p, stream);
-    if (tt * (nw / 128) < sms) return launch_fp4<FMT, 64, true, false>(t, w, tt, p, stream);
-    return launch_fp4<FMT, 128, true, false>(t, w, tt, p, stream);
+    if (V == 1) return launch_fp4<FMT, 64, true, false, true>(t, w, tt, p, stream);
+    if (V == 2) return launch_fp4<FMT, 128, true, false, false>(t, w, tt, p, stream);
+    if (V == 3) return launch_fp4<FMT, 128, true, true, false>(t, w, tiles(256), p, stream);
+    if (3 * tt * (nw / 128) < 2 * sms) return launch_fp4<FMT, 64, true, false, true>(t, w, tt, p, stream);
+    return launch_fp4<FMT, 128, true, false, false>(t, w, tt, p, stream);
   } else {
-    if (V == 1) return launch_fp4<FMT, 64, false, false>(t, w, tt, p, stream);
-    if (V == 2) return launch_fp4<FMT, 128, false, false>(t, w, tt, p, stream);
-    if (V == 3) return launch_fp4<FMT, 256, false, true>(t, w, tiles(256), p, stream);
-    if (V == 4) return launch_fp4<FMT, 256, false, false>(t, w, tt, p, stream);
-    if (tt * ((nw + 127) / 128) < sms || (per <= 64 && !p.offsets && V == 0)) return launch_fp4<FMT, 64, false, false>(t, w, tt, p, stream);
-    if (!p.offsets && tiles(256) * ((nw + 255) / 256) >= sms / 2)
-      return launch_fp4<FMT, 256, false, true>(t, w, tiles(256), p, stream);
-    if (tt * ((nw + 255) / 256) < sms) return launch_fp4<FMT, 128, false, false>(t, w, tt, p, stream);
-    return launch_fp4<FMT, 256, false, false>(t, w, tt, p, stream);
+    if (V == 1) return launch_fp4<FMT, 128, false, false, true>(t, w, tt, p, stream);
+    if (V == 2) return launch_fp4<FMT, 128, false, false, false>(t, w, tt, p, stream);
+    if (V == 3) return launch_fp4<FMT, 256, false, true, false>(t, w, tiles(256), p, stream);
+    if (V == 4) return launch_fp4<FMT, 256, false, false, false>(t, w, tt, p, stream);
+    const int64_t u128 = tt * ((nw + 127) / 128), u256 = tt * ((nw + 255) / 256);
+    if (V == 9 || u128 <= sms / 2 || (u128 < sms && per <= 64)) return launch_fp4<FMT, 128, false, false, true>(t, w, tt, p, stream);
+    if (!p.offsets && tiles(256) * ((nw + 255) / 256) >= sms / 2 && p.M > 128)
+      return launch_fp4<FMT, 256, false, true, false>(t, w, tiles(256), p, stream);
+    if (2 * ((u256 + sms - 1) / sms) > (u128 + sms - 1) / sms) return launch_fp4<FMT, 128, false, false, false>(t, w, tt, p, stream);
+    return launch_fp4<FMT, 256, false, false, false>(t, w, tt, p, stream);
   }
 }
 
