@@ -24,7 +24,6 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
-#include <cstdlib>
 #include <mutex>
 
 #include "fp8q_common.cuh"
@@ -110,6 +109,20 @@ __device__ __forceinline__ void arrive_relaxed(uint32_t bar_cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
 }
 
+// Whether a barrier's phase is complete, without waiting: test_wait, since
+// try_wait suspends the warp for microseconds when it is not.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // A 512-byte scale block -- 32 rows of 16 bytes, row l the scales of operand
 // rows l, l + 32, l + 64, l + 96 -- from shared memory into 4 columns of all
 // four lane quadrants of tensor memory (of both CTAs, each from its own shared
@@ -139,14 +152,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// A value that all lanes of the warp hold, in a uniform register: what comes
+// from shared memory the compiler must take for different in every lane, and
+// then every address and loop that depends on it too.  A warp reduction's
+// result it knows to be uniform.  (A stage's two copies took ~430 cycles to
+// issue without it.)
+__device__ __forceinline__ int uniform(int v) {
+  return static_cast<int>(__reduce_or_sync(0xFFFFFFFFu, static_cast<unsigned>(v)));
+}
+
 // A tile: its expert, first token row and how many rows are the expert's, the
 // token scales' block row, and the first weight row (of the expert).
 struct Fp4Tile {
-  int e;
-  int t0;
-  int cnt;
-  int64_t tblk;
-  int64_t n0;
+  int e, t0, cnt, tblk, n0;
 };
 
 // What a CTA keeps of an expert in shared memory (read once, so that a tile
@@ -156,57 +174,60 @@ struct Fp4Expert {
   int tiles, first, rows, sf;
 };
 
-// Tile u: an expert's tiles are consecutive, its token tiles the fastest index
-// (they share the weight tile, which then comes from L2).  A CTA pair's tile
-// has 256 token rows; `rank` says which 128 of them.
+// Tile u (the whole warp calls): an expert's tiles are consecutive, its token
+// tiles the fastest index (they share the weight tile, which then comes from
+// L2).  A CTA pair's tile has 256 token rows; `rank` says which 128 of them.
 template <bool PAIR>
 __device__ __forceinline__ Fp4Tile fp4_tile(const Fp4Args& p, const Fp4Expert* ex, int u, int tn, int rank) {
   constexpr int TM = PAIR ? 256 : 128;
-  int lo = 0, hi = p.E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ex[mid].tiles * p.tiles_n <= u) lo = mid; else hi = mid;
+  int lo = 0;
+  if (p.E > 1) {
+    // the last expert with no more than u tiles before it, in steps of 32 and of 1
+    const int lane = threadIdx.x & 31, step = (p.E + 31) >> 5;
+    const int e = lane * step;
+    lo = (__popc(__ballot_sync(0xFFFFFFFFu, e < p.E && ex[e < p.E ? e : 0].tiles * p.tiles_n <= u)) - 1) * step;
+    const int f = lo + lane;
+    const bool in = lane < step && f < p.E;
+    lo += __popc(__ballot_sync(0xFFFFFFFFu, in && ex[in ? f : 0].tiles * p.tiles_n <= u)) - 1;
   }
-  const Fp4Expert x = ex[lo];
+  lo = uniform(lo);
+  const Fp4Expert x = {uniform(ex[lo].tiles), uniform(ex[lo].first), uniform(ex[lo].rows), uniform(ex[lo].sf)};
   const int mt = (x.rows + TM - 1) / TM;
   const int r = u - x.tiles * p.tiles_n;
-  const int nt = mt == 1 ? r : r / mt, m = r - nt * mt;
+  const int nt = mt == 1 ? r : uniform(r / mt), m = r - nt * mt;
   const int b = PAIR ? 2 * m + rank : m;
   Fp4Tile t;
   t.e = lo;
   t.t0 = x.first + 128 * b;
   t.cnt = max(0, min(128, x.rows - 128 * b));
   t.tblk = x.sf + b;
-  t.n0 = static_cast<int64_t>(nt) * tn;
+  t.n0 = nt * tn;
   return t;
 }
 
 // ------------------------------------------------------------------- kernel
-// CH output columns a tile: 128 or 256 weight rows, or FUSED 64 or 128 hidden
-// channels, whose gate rows are followed by the up rows.  128 channels are one
-// 256-column MMA, 64 are two 64-column ones (gate, up), each with the scale
-// block that its rows lie in; a tile that begins in the middle of a block finds
-// its scales two tensor memory columns further.  SPLIT: one tile a cluster,
-// whose CTAs share its depth.  PAIR: two CTAs of a cluster share one MMA
-// of 256 token rows and 256 columns (tcgen05 cta_group::2), each with 128 of
-// the rows of both operands in its shared memory, so a weight row reaches each
-// SM half as often; each holds the scales of its own tokens and of all columns.
-// Tried and slower: a tile as two 128-column MMAs and accumulators, so that one
-// is read while the other computes (a pair's 128-column MMA took ~140 cycles,
-// more than the 256-column one: 1341 against 894 us at 8192 x 51200 x 5120).
+// CH output columns a tile: 128 or 256 weight rows, or FUSED 128 hidden
+// channels, whose 128 gate rows are followed by the up rows.
+// PAIR: two CTAs of a cluster share one MMA of 256 token rows and 256 columns
+// (tcgen05 cta_group::2), each with 128 of the rows of both operands in its
+// shared memory, so a weight row reaches each SM half as often; each holds the
+// scales of its own tokens and of all columns.  Tried and slower: a tile as two
+// 128-column MMAs and accumulators, so that one is read while the other
+// computes (a pair's 128-column MMA took ~140 cycles, more than the 256-column
+// one: 1341 against 894 us at 8192 x 51200 x 5120).
+// SPLIT: one tile of 128 weight rows a cluster, whose CTAs share its depth;
+// FUSED, half of them take the gate rows and half the up rows.
 template <int FMT, int CH, bool FUSED, bool PAIR, bool SPLIT>
 struct Fp4Cfg {
   static constexpr int PER_SM = SPLIT ? 2 : 1;              // CTAs on an SM, by tensor memory
-  static constexpr int BN = FUSED ? 2 * CH : CH;            // accumulator columns
-  static constexpr bool TWO_MMA = FUSED && CH == 64;
-  static constexpr int MMA_N = TWO_MMA ? CH : BN;
-  static constexpr int EPI_WARPS = SPLIT && !FUSED ? 4 : 8;
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int HALVES = SPLIT && FUSED ? 2 : 1;     // CTAs for gate and up
+  static constexpr int BN = FUSED ? 2 * CH / HALVES : CH;   // accumulator columns
+  static constexpr int EPI_WARPS = SPLIT ? 4 : 8;
+  static constexpr int THREADS = 96 + 32 * EPI_WARPS;
   static constexpr int NKB = FMT == kNv ? 4 : 2;            // scale blocks of a stage, per 128 rows
   static constexpr int SF_BYTES = NKB * 512;                // per 128 rows
   static constexpr int SF_COLS = NKB * 4;
-  static constexpr int BBLK = FUSED || BN == 256 ? 2 : 1;   // 128-row blocks of weight scales
-  static constexpr int BBOX = FUSED ? CH : (BN < 128 ? BN : 128);   // weight rows of one copy
+  static constexpr int BBLK = BN / 128;                     // 128-row blocks of weight rows
   static constexpr int B_BYTES = (PAIR ? 128 : BN) * kStageBytes;
   static constexpr int SF_STAGE = (1 + BBLK) * SF_BYTES;
   static constexpr int SF_TMEM = (1 + BBLK) * SF_COLS;      // tensor memory columns of a stage's scales
@@ -216,14 +237,9 @@ struct Fp4Cfg {
   static constexpr int TMEM = 512 / PER_SM;
   static constexpr bool STAGED = !FUSED && !SPLIT;          // y leaves through shared memory
   static constexpr int OUT_BYTES = STAGED ? EPI_WARPS * 4096 : 0;
-  // tensor memory columns of the weight scales: from one K block to the next, and between their
-  // 128-row blocks (side by side for one 256-column MMA)
-  static constexpr int B_STEP = MMA_N == 256 ? 8 : 4;
-  static constexpr int B_BLOCK = MMA_N == 256 ? 4 : SF_COLS;
-  // a 64-column MMA of the upper half of a block reads two columns further
-  static_assert(ACC_COLS + SFBUF * SF_TMEM + 2 <= TMEM, "tensor memory");
-  static_assert(!PAIR || (BN == 256 && !SPLIT), "pairs have 256 columns");
-  static_assert(CH >= 128 || (FUSED && SPLIT), "64 channels: split tiles");
+  static_assert(ACC_COLS + SFBUF * SF_TMEM <= TMEM, "tensor memory");
+  static_assert(!PAIR || (BN == 256 && !SPLIT && !FUSED), "pairs: dense, 256 columns");
+  static_assert(!SPLIT || BN == 128, "split tiles have 128 columns");
 };
 
 template <int FMT, int CH, bool FUSED, bool PAIR, bool SPLIT>
@@ -251,15 +267,16 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
   int* all_tiles = reinterpret_cast<int*>(tmem_slot + 2);
   Fp4Expert* ex = reinterpret_cast<Fp4Expert*>(drain + 4);              // [E]
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   // the tile loop: first tile and step; SPLIT: one tile, of whose depth this
-  // CTA takes stages [k0, k1)
-  const int group = SPLIT ? p.split : PAIR ? 2 : 1;
-  const int cta = static_cast<int>(blockIdx.x) / group, ctas = static_cast<int>(gridDim.x) / group;
+  // CTA takes stages [k0, k1), of the gate or the up rows (half)
+  const int group = SPLIT ? p.split * C::HALVES : PAIR ? 2 : 1;
+  const int cta = uniform(static_cast<int>(blockIdx.x) / group), ctas = uniform(static_cast<int>(gridDim.x) / group);
   const int part = SPLIT ? static_cast<int>(blockIdx.x) - cta * group : 0;
-  const int k0 = SPLIT ? p.kstages * part / p.split : 0;
-  const int k1 = SPLIT ? p.kstages * (part + 1) / p.split : p.kstages;
+  const int half = C::HALVES == 2 && part >= p.split ? 1 : 0, kpart = part - half * p.split;
+  const int k0 = SPLIT ? uniform(p.kstages * kpart / p.split) : 0;
+  const int k1 = SPLIT ? uniform(p.kstages * (kpart + 1) / p.split) : p.kstages;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -336,159 +353,168 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
   griddep_launch_dependents();             // this CTA has its tensor memory: a dependent cannot take it first
   if constexpr (PAIR) cluster_sync();      // both CTAs' barriers are ready
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int units = *all_tiles * p.tiles_n;
+  const uint32_t tmem = static_cast<uint32_t>(uniform(static_cast<int>(*tmem_slot)));
+  const int units = uniform(*all_tiles) * p.tiles_n;
 
+  // SPLIT: the tile, and the factors that its output takes, before the long wait
+  Fp4Tile tile0{};
+  const float gh = FUSED && p.gh ? *p.gh : 1.0f;
+  const float ga = p.ga ? *p.ga : 1.0f;
+  float gb = 1.0f;
+  if (SPLIT && cta < units) {
+    tile0 = fp4_tile<PAIR>(p, ex, cta, CH, 0);
+    if (p.gb) gb = p.gb[tile0.e];
+  }
   // a wait by the whole warp; false in all lanes if one gave up
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.status)) != 0;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    {
-      int it = 0, st = 0;
-      uint32_t parity = 1;
-      bool ok = true;
-      for (int u = cta; ok && u < units; u += ctas) {
-        const Fp4Tile t = fp4_tile<PAIR>(p, ex, u, CH, rank);
-        const int wrow = static_cast<int>(t.e * p.N + t.n0);
-        const int up = FUSED ? static_cast<int>(p.I) : 128;       // from the first 128 weight rows to the second
-        const int pieces = (t.cnt + p.box - 1) / p.box;
-        const int64_t wblk = t.e * p.wblocks + (t.n0 >> 7);
-        const uint8_t* sft = p.sft + t.tblk * p.kb * 512;
-        const uint8_t* sfw = p.sfw + wblk * p.kb * 512;
-        // a second block of weight scales: the up half's, or columns 128..255
-        const int64_t second = static_cast<int64_t>(up >> 7) * p.kb * 512;
-        const bool two = FUSED || (BN == 256 && t.n0 + 128 < p.N);
-        int pair_pieces = 0;                                      // of both CTAs, and which have token scales
-        if constexpr (PAIR) {
-          const int other = rank ? 128 : max(0, fp4_tile<PAIR>(p, ex, u, CH, 1).cnt);
-          pair_pieces = pieces + (other + p.box - 1) / p.box;
-        }
-        for (int kb = k0; kb < k1; ++kb) {
-          if (!warp_wait(&empty[st], parity)) { ok = false; break; }
-          uint8_t* a = sA + st * p.a_bytes;
-          uint8_t* b = sB + st * C::B_BYTES;
-          uint8_t* s = sSF + st * C::SF_STAGE;
-          const int x = kb * kStageBytes;
-          if (elect_one()) {
-            if constexpr (PAIR) {
-              // everything lands on the even CTA's barrier; boxes reaching past a matrix count in full
-              if (rank == 0)
-                mbar_arrive_expect_tx(&full[st], pair_pieces * p.box * kStageBytes + 2 * C::B_BYTES + 6 * C::SF_BYTES);
-              const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
-              const int y = kb * C::NKB;
-              tma_load_2d_pair(b, &tmW, bar, x, wrow + (rank ? up : 0));
+  if (warp == 0 || warp == 2 + C::EPI_WARPS) {
+    // ------------------------------------------------------------ producers
+    // One warp copies weights and their scales, another the tokens' (four
+    // copies a stage by one warp took as long as the stage's MMAs).  The first
+    // announces a stage's bytes; the barrier cannot complete before it does.
+    const bool tokens = warp != 0;
+    int it = 0, st = 0;
+    uint32_t parity = 1;
+    bool ok = true;
+    for (int u = cta; ok && u < units; u += ctas) {
+      const Fp4Tile t = fp4_tile<PAIR>(p, ex, u, CH, rank);
+      const int up = FUSED ? static_cast<int>(p.I) : 128;       // from the first 128 weight rows to the second
+      const int wrow = t.e * static_cast<int>(p.N) + t.n0 + (PAIR ? rank : half) * up;
+      const int pieces = (t.cnt + p.box - 1) / p.box;
+      const int64_t wblk = t.e * p.wblocks + ((t.n0 + half * up) >> 7);
+      const uint8_t* sft = p.sft + static_cast<int64_t>(t.tblk) * p.kb * 512;
+      const uint8_t* sfw = p.sfw + wblk * p.kb * 512;
+      // a second block of weight scales: the up half's, or columns 128..255
+      const int64_t second = static_cast<int64_t>(up >> 7) * p.kb * 512;
+      const bool two = C::BBLK == 2 && (FUSED || t.n0 + 128 < p.N);
+      // bytes of a stage beside the scales: of both CTAs of a pair, whose boxes count in full
+      int bytes = pieces * p.box * kStageBytes + C::B_BYTES;
+      if constexpr (PAIR) {
+        const int other = fp4_tile<PAIR>(p, ex, u, CH, 1).cnt;
+        bytes += (other + p.box - 1) / p.box * p.box * kStageBytes + C::B_BYTES + 6 * C::SF_BYTES;
+      }
+      bool ready = mbar_test(&empty[st], parity);
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!__all_sync(0xFFFFFFFFu, ready) && !warp_wait(&empty[st], parity)) { ok = false; break; }
+        const int cur = st;
+        ++it;
+        if (++st == S) { st = 0; parity ^= 1u; }
+        ready = mbar_test(&empty[st], parity);              // the next stage's, while this one is issued
+        uint8_t* a = sA + cur * p.a_bytes;
+        uint8_t* b = sB + cur * C::B_BYTES;
+        uint8_t* s = sSF + cur * C::SF_STAGE;
+        const int x = kb * kStageBytes;
+        const uint32_t sfb = min(C::NKB, p.kb - kb * C::NKB) * 512;
+        const int64_t sfo = static_cast<int64_t>(kb) * C::SF_BYTES;
+        if (elect_one()) {
+          if constexpr (PAIR) {
+            // everything lands on the even CTA's barrier
+            const uint32_t bar = mapa_shared(smem_u32(&full[cur]), 0);
+            const int y = kb * C::NKB;
+            if (!tokens) {
+              if (rank == 0) mbar_arrive_expect_tx(&full[cur], bytes);
+              tma_load_2d_pair(b, &tmW, bar, x, wrow);
               tma_load_2d_pair(s + C::SF_BYTES, &tmWS, bar, 0, static_cast<int>(wblk) * p.kb + y);
               tma_load_2d_pair(s + 2 * C::SF_BYTES, &tmWS, bar, 0, static_cast<int>(wblk + (up >> 7)) * p.kb + y);
+            } else {
               for (int i = 0; i < pieces; ++i)
                 tma_load_2d_pair(a + i * p.box * kStageBytes, &tmT, bar, x, t.t0 + i * p.box);
-              tma_load_2d_pair(s, &tmTS, bar, 0, static_cast<int>(t.tblk) * p.kb + y);
-            } else {
-              const uint32_t sfb = min(C::NKB, p.kb - kb * C::NKB) * 512;
-              const int64_t sfo = static_cast<int64_t>(kb) * C::SF_BYTES;
-              mbar_arrive_expect_tx(&full[st], pieces * p.box * kStageBytes + C::B_BYTES + (two ? 3 : 2) * sfb);
-              tma_load_2d(b, &tmW, &full[st], x, wrow);
-              if (C::BBLK == 2) tma_load_2d(b + C::BBOX * kStageBytes, &tmW, &full[st], x, wrow + up);
-              bulk_load(s + C::SF_BYTES, sfw + sfo, sfb, &full[st]);
-              if (two) bulk_load(s + 2 * C::SF_BYTES, sfw + second + sfo, sfb, &full[st]);
-              for (int i = 0; i < pieces; ++i)
-                tma_load_2d(a + i * p.box * kStageBytes, &tmT, &full[st], x, t.t0 + i * p.box);
-              bulk_load(s, sft + sfo, sfb, &full[st]);
+              tma_load_2d_pair(s, &tmTS, bar, 0, t.tblk * p.kb + y);
             }
+          } else if (!tokens) {
+            mbar_arrive_expect_tx(&full[cur], bytes + (two ? 3 : 2) * sfb);
+            tma_load_2d(b, &tmW, &full[cur], x, wrow);
+            if (C::BBLK == 2) tma_load_2d(b + 128 * kStageBytes, &tmW, &full[cur], x, wrow + up);
+            bulk_load(s + C::SF_BYTES, sfw + sfo, sfb, &full[cur]);
+            if (two) bulk_load(s + 2 * C::SF_BYTES, sfw + second + sfo, sfb, &full[cur]);
+          } else {
+            for (int i = 0; i < pieces; ++i)
+              tma_load_2d(a + i * p.box * kStageBytes, &tmT, &full[cur], x, t.t0 + i * p.box);
+            bulk_load(s, sft + sfo, sfb, &full[cur]);
           }
-          __syncwarp();
-          ++it;
-          if (++st == S) { st = 0; parity ^= 1u; }
         }
+        __syncwarp();
       }
-      // let the copies in flight land before this CTA (or its pair) can leave;
-      // at once when everything was consumed
-      const int first = it - S > 0 ? it - S : 0;
-      for (int j = first; (PAIR ? rank == 0 : !ok) && j < it; ++j) drain_wait(&full[j % S], (j / S) & 1);
     }
+    // Let the copies in flight land before this CTA (or its pair) can leave; at
+    // once when everything was consumed.
+    const int first = it - S > 0 ? it - S : 0;
+    for (int j = first; (PAIR ? rank == 0 : !ok) && j < it; ++j) drain_wait(&full[j % S], (j / S) & 1);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (the even CTA's, of a pair)
-    {
-      if (rank == 0) {
-        const uint32_t id0 = idesc_fp4(FMT, PAIR ? 256 : 128, C::MMA_N, 0);
-        auto commit = [](uint64_t* bar) {
-          if constexpr (PAIR) mma_commit_pair(bar, 0x3);
-          else mma_commit(bar);
-        };
-        const uint64_t a_desc = smem_desc_kmajor_sw128(sA), b_desc = smem_desc_kmajor_sw128(sB);
-        const uint64_t sf_desc = scales_desc(sSF);
-        int st = 0, sbuf = 0, buf = 0;
-        uint32_t parity = 0, acc_parity = 1;
-        bool ok = true;
-        for (int u = cta; ok && u < units; u += ctas) {
-          // 64-column tiles: the second half of a 128-row scale block lies two columns on
-          const uint32_t wcol =
-              CH == 64 ? static_cast<uint32_t>((fp4_tile<PAIR>(p, ex, u, CH, 0).n0 & 64) >> 5) : 0u;
-          if (!warp_wait(&tempty[buf], acc_parity)) { ok = false; break; }
+    if (rank == 0) {
+      const uint32_t id0 = idesc_fp4(FMT, PAIR ? 256 : 128, BN, 0);
+      auto commit = [](uint64_t* bar) {
+        if constexpr (PAIR) mma_commit_pair(bar, 0x3);
+        else mma_commit(bar);
+      };
+      const uint64_t a_desc = smem_desc_kmajor_sw128(sA), b_desc = smem_desc_kmajor_sw128(sB);
+      const uint64_t sf_desc = scales_desc(sSF);
+      int st = 0, sbuf = 0, buf = 0;
+      uint32_t parity = 0, acc_parity = 1;
+      bool ok = true;
+      for (int u = cta; ok && u < units; u += ctas) {
+        if (!warp_wait(&tempty[buf], acc_parity)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t d = tmem + buf * BN;
+        bool ready = mbar_test(&full[st], parity);
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!__all_sync(0xFFFFFFFFu, ready) && !warp_wait(&full[st], parity)) { ok = false; break; }
           tc_fence_after();
-          for (int kb = k0; kb < k1; ++kb) {
-            if (!warp_wait(&full[st], parity)) { ok = false; break; }
-            tc_fence_after();
-            const uint32_t sfa = tmem + C::ACC_COLS + sbuf * C::SF_TMEM;
-            const uint32_t sfb = sfa + C::SF_COLS + wcol;
-            const uint64_t sd = sf_desc + static_cast<uint32_t>(st * (C::SF_STAGE >> 4));
-            const uint64_t ad = a_desc + static_cast<uint32_t>(st * (p.a_bytes >> 4));
-            const uint64_t bd = b_desc + static_cast<uint32_t>(st * (C::B_BYTES >> 4));
-            const int nk = p.kb - kb * C::NKB;                       // scale blocks and K slices left
-            const int ks = static_cast<int>((p.K - static_cast<int64_t>(kb) * 256 + 63) >> 6);
-            // the stage's MMAs into columns d: weight rows from descriptor w on, their scales at column sw
-            auto mmas = [&](uint32_t d, uint64_t w, uint32_t sw) {
+          const int cur = st;
+          if (++st == S) { st = 0; parity ^= 1u; }
+          ready = mbar_test(&full[st], parity);             // the next stage's, while this one is issued
+          const uint32_t sfa = tmem + C::ACC_COLS + sbuf * C::SF_TMEM;
+          const uint32_t sfb = sfa + C::SF_COLS;
+          const uint64_t sd = sf_desc + static_cast<uint32_t>(cur * (C::SF_STAGE >> 4));
+          const uint64_t ad = a_desc + static_cast<uint32_t>(cur * (p.a_bytes >> 4));
+          const uint64_t bd = b_desc + static_cast<uint32_t>(cur * (C::B_BYTES >> 4));
+          const int nk = p.kb - kb * C::NKB;                       // scale blocks and K slices left
+          const int ks = static_cast<int>((p.K - static_cast<int64_t>(kb) * 256 + 63) >> 6);
+          if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (k < ks) {
-                  // nvfp4: a K slice has a scale block of its own; mxfp4: two share one, ids 0 and 2
-                  const int b = FMT == kNv ? k : k >> 1;
-                  const uint32_t id = FMT == kNv ? 0u : 2u * (k & 1);
-                  mma_fp4<FMT, PAIR>(d, ad + 2 * k, w + 2 * k, id0 | (id << 4) | (id << 29), kb > k0 || k > 0,
-                                     (sfa + b * 4) | (id << 30), (sw + b * C::B_STEP) | (id << 30));
-                }
+            for (int b = 0; b < C::NKB; ++b) {
+              if (b < nk) {
+                cp_scales<PAIR>(sfa + b * 4, sd + (b * 512 >> 4));
+#pragma unroll
+                for (int j = 0; j < C::BBLK; ++j)
+                  cp_scales<PAIR>(sfb + b * (4 * C::BBLK) + j * 4, sd + (((1 + j) * C::SF_BYTES + b * 512) >> 4));
               }
-            };
-            if (elect_one()) {
-#pragma unroll
-              for (int b = 0; b < C::NKB; ++b) {
-                if (b < nk) {
-                  cp_scales<PAIR>(sfa + b * 4, sd + (b * 512 >> 4));
-#pragma unroll
-                  for (int j = 0; j < C::BBLK; ++j)
-                    cp_scales<PAIR>(sfa + C::SF_COLS + b * C::B_STEP + j * C::B_BLOCK,
-                                    sd + (((1 + j) * C::SF_BYTES + b * 512) >> 4));
-                }
-              }
-              const uint32_t d = tmem + buf * BN;
-              mmas(d, bd, sfb);
-              if constexpr (C::TWO_MMA) mmas(d + CH, bd + (CH * kStageBytes >> 4), sfb + C::B_BLOCK);
-              commit(&empty[st]);
-              if (kb + 1 == k1) commit(&tfull[buf]);
             }
-            __syncwarp();
-            if (++st == S) { st = 0; parity ^= 1u; }
-            if (++sbuf == C::SFBUF) sbuf = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k < ks) {
+                // nvfp4: a K slice has a scale block of its own; mxfp4: two share one, ids 0 and 2
+                const int b = FMT == kNv ? k : k >> 1;
+                const uint32_t id = FMT == kNv ? 0u : 2u * (k & 1);
+                mma_fp4<FMT, PAIR>(d, ad + 2 * k, bd + 2 * k, id0 | (id << 4) | (id << 29), kb > k0 || k > 0,
+                                   (sfa + b * 4) | (id << 30), (sfb + b * (4 * C::BBLK)) | (id << 30));
+              }
+            }
+            commit(&empty[cur]);
+            if (kb + 1 == k1) commit(&tfull[buf]);
           }
-          if (++buf == NB) { buf = 0; acc_parity ^= 1u; }
+          __syncwarp();
+          if (++sbuf == C::SFBUF) sbuf = 0;
         }
-        // every MMA issued has completed once `drain` flips
-        if (elect_one()) commit(drain);
+        if (++buf == NB) { buf = 0; acc_parity ^= 1u; }
       }
-      drain_wait(drain, 0);
+      // every MMA issued has completed once `drain` flips
+      if (elect_one()) commit(drain);
+      __syncwarp();
     }
+    drain_wait(drain, 0);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3;                        // tensor memory lanes 32 quad ..
     const int r = quad * 32 + lane;                   // this thread's token of the tile
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
-    const float ga = p.ga ? *p.ga : 1.0f;
-    const float gh = FUSED && p.gh ? *p.gh : 1.0f;
-    constexpr int COLS = CH / (C::EPI_WARPS / 4);     // output columns of a thread
+    constexpr int COLS = CH / (C::EPI_WARPS / 4);     // output columns of a thread (not SPLIT)
     const int col0 = ((warp - 2) >> 2) * COLS;
     const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
     // the accumulator goes back to the MMAs (of the even CTA)
@@ -500,32 +526,34 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
         else mbar_arrive(&tempty[buf]);
       }
     };
-    // 32 columns of this CTA's part of a split tile, fp32, over the ring (whose
-    // copies and MMAs are done): row r at r BN, 16-byte chunks XORed by the row
-    auto keep_part = [&](uint32_t acc, int col, int row) {
-      uint32_t v[32];
-      tmem_ld_waited<32>(acc, v);
-      uint4* d = reinterpret_cast<uint4*>(smem + row * (BN * 4));
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        d[(col / 4 + i) ^ (row & 7)] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    };
     int buf = 0;
     uint32_t parity = 0;
     bool ok = true;
     for (int u = cta; ok && u < units; u += ctas) {
-      const Fp4Tile t = fp4_tile<PAIR>(p, ex, u, CH, rank);
-      const float alpha = p.gb ? ga * p.gb[t.e] : ga;
-      if constexpr (!FUSED) {
-        if (!warp_wait(&tfull[buf], parity)) { ok = false; break; }
+      const Fp4Tile t = SPLIT ? tile0 : fp4_tile<PAIR>(p, ex, u, CH, rank);
+      if (!SPLIT && p.gb) gb = p.gb[t.e];      // on its way while the tile is computed
+      if constexpr (SPLIT) {
+        // This CTA's part of the tile, fp32, over the ring (whose copies and MMAs
+        // are done): row r at r BN, 16-byte chunks XORed by the row.
+        if (!warp_wait(&tfull[0], parity)) { ok = false; break; }
         tc_fence_after();
-        if (SPLIT && p.split > 1) {
-          if (quad * 32 < t.cnt) {
+        constexpr int PART = BN / (C::EPI_WARPS / 4);
+        if (quad * 32 < t.cnt) {
+#pragma unroll 1
+          for (int c = 0; c < PART; c += 32) {
+            const int col = ((warp - 2) >> 2) * PART + c;
+            uint32_t v[32];
+            tmem_ld_waited<32>(tmem + lane_addr + col, v);
+            uint4* d = reinterpret_cast<uint4*>(smem + r * (BN * 4));
 #pragma unroll
-            for (int c = 0; c < COLS; c += 32) keep_part(tmem + lane_addr + col0 + c, col0 + c, r);
+            for (int i = 0; i < 8; ++i)
+              d[(col / 4 + i) ^ (r & 7)] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
-          continue;
         }
+      } else if constexpr (!FUSED) {
+        if (!warp_wait(&tfull[buf], parity)) { ok = false; break; }
+        const float alpha = ga * gb;
+        tc_fence_after();
         // The thread's columns, rounded to bf16 as they are read (the next 32 in
         // flight meanwhile), so that the accumulator goes back to the MMAs
         // before anything is stored.
@@ -547,7 +575,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
         give_back(buf);
         if (++buf == NB) { buf = 0; parity ^= 1u; }
         const int64_t n = t.n0 + col0;
-        if constexpr (C::STAGED) {
+        {
           // A lane's row of 64 columns (128 bytes) through shared memory, 16-byte
           // chunks XORed by the row, so that eight lanes store a whole line of y:
           // stored from the lane that holds it, a 32-byte piece costs a line's
@@ -571,28 +599,16 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
                       *reinterpret_cast<const uint4*>(mine + i * 128 + (((lane ^ i) & 7) << 4));
             }
           }
-        } else if (r < t.cnt) {
-          uint16_t* y = p.y + static_cast<int64_t>(t.t0 + r) * p.ldy + n;
-#pragma unroll
-          for (int c = 0; c < COLS / 2; c += 4)
-            if (n + 2 * c < p.N)
-              *reinterpret_cast<uint4*>(y + 2 * c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
         }
       } else {
         // The same gate and up columns of the thread's row; the accumulator
         // goes back once they are in registers.
         if (!warp_wait(&tfull[0], parity)) { ok = false; break; }
+        const float alpha = ga * gb;
         parity ^= 1u;
         tc_fence_after();
         const uint32_t acc = tmem + lane_addr + col0;
         const int64_t n = t.n0 + col0;
-        if (SPLIT && p.split > 1) {
-          if (quad * 32 < t.cnt) {
-            keep_part(acc, col0, r);
-            keep_part(acc + CH, CH + col0, r);
-          }
-          continue;
-        }
         uint32_t g[COLS], w[COLS];
         if (quad * 32 < t.cnt) {
 #pragma unroll
@@ -628,7 +644,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
           for (int c = 0; c < COLS / 8; c += 4)
             q[c / 4] = make_uint4(code[c], code[c + 1], code[c + 2], code[c + 3]);
           // tiles begin at a block row of the scales; a thread's scales are aligned 1 to 4 bytes of a word
-          uint8_t* sf = p.hsf + fp4_sf_offset(t.tblk * 128 + r, n / G, fp4_kblocks(FMT, p.I));
+          uint8_t* sf = p.hsf + fp4_sf_offset(static_cast<int64_t>(t.tblk) * 128 + r, n / G, fp4_kblocks(FMT, p.I));
           if constexpr (COLS / G == 4) *reinterpret_cast<uint32_t*>(sf) = sfw;
           else if constexpr (COLS / G == 2) *reinterpret_cast<uint16_t*>(sf) = static_cast<uint16_t>(sfw);
           else *sf = static_cast<uint8_t>(sfw);
@@ -638,53 +654,64 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
   }
 
   if constexpr (SPLIT) {
-    if (p.split > 1) {
-      // The cluster's parts, added in the order of the depth; its CTAs take
-      // turns at groups of G neighbouring outputs of a row.
-      cluster_sync();
-      if (cta < units && *abort_flag == 0) {
-        constexpr int G = FUSED ? fp4_group<FMT>() : 8;
-        const Fp4Tile t = fp4_tile<PAIR>(p, ex, cta, CH, 0);
-        const float alpha = (p.ga ? *p.ga : 1.0f) * (p.gb ? p.gb[t.e] : 1.0f);
-        for (int i = part * C::THREADS + threadIdx.x; i < t.cnt * (CH / G); i += p.split * C::THREADS) {
-          const int row = i / (CH / G), col = (i - row * (CH / G)) * G;
-          float v[FUSED ? 2 * G : G] = {};
+    // The parts of the cluster's CTAs, added in the order of the depth.  Its
+    // warps take turns at pieces of a row: 32 hidden channels, a lane each, or
+    // 32 chunks of 8 outputs (two rows, one, or part of one).
+    cluster_sync();
+    if (cta < units && *abort_flag == 0) {
+      const Fp4Tile& t = tile0;
+      const float alpha = ga * gb;
+      constexpr int WARPS = C::THREADS / 32, UNIT = FUSED ? 1 : 8, PIECES = CH / UNIT;   // of a row
+      for (int i0 = (part * WARPS + warp) * 32; i0 < t.cnt * PIECES; i0 += group * WARPS * 32) {
+        const int row = (i0 + lane) / PIECES, col = (i0 + lane - row * PIECES) * UNIT;
+        float v[FUSED ? 2 : 8] = {};
+        if (row < t.cnt) {
           for (int q = 0; q < p.split; ++q) {
             const uint32_t src = mapa_shared(smem_u32(smem), q) + row * (BN * 4);
-#pragma unroll
-            for (int j = 0; j < (FUSED ? 2 * G : G); j += 4) {
-              const int c = j < G ? col + j : CH + col + j - G;
-              float f[4];
+            const uint32_t at = src + (((col >> 2) ^ (row & 7)) << 4);
+            if constexpr (FUSED) {
+              float g, u;
+              asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(g) : "r"(at + 4 * (col & 3)) : "memory");
+              const uint32_t upper = mapa_shared(smem_u32(smem), p.split + q) + (at - mapa_shared(smem_u32(smem), q));
+              asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u) : "r"(upper + 4 * (col & 3)) : "memory");
+              v[0] += g;
+              v[1] += u;
+            } else {
+              float f[8];
               asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                           : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
-                           : "r"(src + (((c / 4) ^ (row & 7)) << 4))
-                           : "memory");
+                           : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(at) : "memory");
+              asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                           : "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                           : "r"(src + ((((col >> 2) + 1) ^ (row & 7)) << 4)) : "memory");
 #pragma unroll
-              for (int k = 0; k < 4; ++k) v[j + k] += f[k];
+              for (int k = 0; k < 8; ++k) v[k] += f[k];
             }
-          }
-          const int64_t n = t.n0 + col;
-          if constexpr (FUSED) {
-            float y[G], amax = 0.0f;
-#pragma unroll
-            for (int j = 0; j < G; ++j) {
-              y[j] = silu_mul_f32(v[j] * alpha, v[G + j] * alpha);
-              amax = fmaxf(amax, fabsf(y[j]));
-            }
-            const Fp4Scale sc = fp4_scale<FMT>(amax, p.gh ? *p.gh : 1.0f);
-            uint32_t* q = reinterpret_cast<uint32_t*>(p.hq + static_cast<int64_t>(t.t0 + row) * (p.I >> 1) + (n >> 1));
-#pragma unroll
-            for (int j = 0; j < G; j += 8) q[j / 8] = fp4_codes8<FMT>(y + j, sc);
-            p.hsf[fp4_sf_offset(t.tblk * 128 + row, n / G, fp4_kblocks(FMT, p.I))] = static_cast<uint8_t>(sc.byte);
-          } else if (n < p.N) {
-            *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(t.t0 + row) * p.ldy + n) =
-                make_uint4(pack_bf16(v[0] * alpha, v[1] * alpha), pack_bf16(v[2] * alpha, v[3] * alpha),
-                           pack_bf16(v[4] * alpha, v[5] * alpha), pack_bf16(v[6] * alpha, v[7] * alpha));
           }
         }
+        const int64_t n = t.n0 + col;
+        if constexpr (FUSED) {
+          // whole warps: the channels of a row are four warps' worth
+          constexpr int G = fp4_group<FMT>();
+          const float y = silu_mul_f32(v[0] * alpha, v[1] * alpha);
+          float amax = fabsf(y);
+#pragma unroll
+          for (int o = G / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          const Fp4Scale sc = fp4_scale<FMT>(amax, gh);
+          uint32_t code = fp4_code1<FMT>(y, sc) << (4 * (lane & 7));
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) code |= __shfl_xor_sync(0xFFFFFFFFu, code, o);
+          if ((lane & 7) == 0)
+            *reinterpret_cast<uint32_t*>(p.hq + static_cast<int64_t>(t.t0 + row) * (p.I >> 1) + (n >> 1)) = code;
+          if (lane % G == 0)
+            p.hsf[fp4_sf_offset(static_cast<int64_t>(t.tblk) * 128 + row, n / G, fp4_kblocks(FMT, p.I))] = static_cast<uint8_t>(sc.byte);
+        } else if (row < t.cnt && n < p.N) {
+          *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(t.t0 + row) * p.ldy + n) =
+              make_uint4(pack_bf16(v[0] * alpha, v[1] * alpha), pack_bf16(v[2] * alpha, v[3] * alpha),
+                         pack_bf16(v[4] * alpha, v[5] * alpha), pack_bf16(v[6] * alpha, v[7] * alpha));
+        }
       }
-      cluster_sync();                        // no part is given up while another CTA reads it
     }
+    cluster_sync();                          // no part is given up while another CTA reads it
   }
   tc_fence_before();
   __syncthreads();
@@ -750,11 +777,11 @@ template <int FMT, int CH, bool FUSED, bool PAIR, bool SPLIT>
 fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p, cudaStream_t stream) {
   using C = Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>;
   CUtensorMap mt, mw, mts, mws;
-  if (!fp4_tensor_map(t, p.M, p.K, p.box, &mt) || !fp4_tensor_map(w, p.E * p.N, p.K, C::BBOX, &mw))
+  if (!fp4_tensor_map(t, p.M, p.K, p.box, &mt) || !fp4_tensor_map(w, p.E * p.N, p.K, 128, &mw))
     return FP8Q_ERR_CUDA;
   if (PAIR) {
-    const int64_t tblocks = p.offsets ? p.M / 128 + (p.M < p.E ? p.M : p.E) : (p.M + 127) / 128;
-    if (!fp4_scale_map(p.sft, tblocks * p.kb, C::NKB, &mts) || !fp4_scale_map(p.sfw, p.E * p.wblocks * p.kb, C::NKB, &mws))
+    if (!fp4_scale_map(p.sft, (p.M + 127) / 128 * p.kb, C::NKB, &mts) ||
+        !fp4_scale_map(p.sfw, p.wblocks * p.kb, C::NKB, &mws))
       return FP8Q_ERR_CUDA;
   } else {
     mts = mt;      // not read
@@ -778,13 +805,12 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
     // least.  (More and shorter parts were slower: 1 x 5120 x 25600 nvfp4 took
     // 18.1 us in 3 parts, 19.2 in 4; clusters that do not fit at once wait for
     // the first to end, so split tiles leave room for two CTAs on an SM.)
-    p.split = static_cast<int>(units > 0 ? num_sms() / units : 1);
-    if (p.split > 8) p.split = 8;
+    p.split = static_cast<int>(units > 0 ? num_sms() / (units * C::HALVES) : 1);
+    if (p.split > 8 / C::HALVES) p.split = 8 / C::HALVES;
     if (p.split > p.kstages / 2) p.split = p.kstages / 2;
     if (p.split < 1) p.split = 1;
-    { const char* e = getenv("SPL"); if (e && atoi(e)) p.split = atoi(e); }
-    if (units * p.split > num_sms() || p.split > 1) per_sm = 2;
-    if (p.split > 1) part = (p.M < 128 ? static_cast<int>(p.M + 31) / 32 * 32 : 128) * C::BN * 4;
+    if (units * p.split * C::HALVES > num_sms() || p.split * C::HALVES > 1) per_sm = 2;
+    part = (p.M < 128 ? static_cast<int>(p.M + 31) / 32 * 32 : 128) * C::BN * 4;
   }
   p.stages = stages(per_sm);
   p.ring = p.stages * stage;
@@ -822,40 +848,40 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
     attr_done[dev].store(fit, std::memory_order_relaxed);
   }
   if (SPLIT)
-    return launch_kernel(kern, dim3(static_cast<unsigned>(units * p.split)), dim3(C::THREADS), smem, stream, p.split,
-                         mt, mw, mts, mws, p);
+    return launch_kernel(kern, dim3(static_cast<unsigned>(units * p.split * C::HALVES)), dim3(C::THREADS), smem, stream,
+                         p.split * C::HALVES, mt, mw, mts, mws, p);
   const unsigned grid = static_cast<unsigned>(units < fit ? units : fit) * (PAIR ? 2 : 1);
   return launch_kernel(kern, dim3(grid), dim3(C::THREADS), smem, stream, PAIR ? 2 : 1, mt, mw, mts, mws, p);
 }
 
-// Variant and launch.
+// Variant and launch, by how many tiles there are for the SMs.  Measured on
+// both sides of each border (us):
+//   split tiles up to half as many 128-row tiles as SMs: 16 x 4096 x 12288
+//     mxfp4 (32 tiles) 9.7 split, 18.5 not; 1 x 10240 x 5120 (80) 11.2 and 11.0
+//   CTA pairs from as many 256 x 256 tiles as pairs of SMs: 512 x 10240 x 5120
+//     nvfp4 (80) 22.2 in pairs, 25.0 with 128 rows, 25.5 with 256; 256 x 5120 x
+//     5120 (20) 13, 10.6 and 12.9.  Experts' rows are ragged: pairs lost or
+//     drew everywhere (256 rows an expert, gate_up 88 in pairs, 83 without)
+//   256 weight rows unless 128 spread over the SMs in less than twice as many
+//     rounds: 1 x 51200 x 5120 (400 tiles of 128: 3 rounds, 200 of 256: 2) 29.4
+//     with 256, 26.2 with 128; 1 x 24576 x 4096 (2 and 1) 14.2 and 16.9
 template <int FMT, bool FUSED>
 fp8q_status run_fp4(const void* t, const void* w, Fp4Args& p, cudaStream_t stream) {
+  const int64_t sms = num_sms(), nw = FUSED ? p.I : p.N;
+  auto rounds = [&](int64_t tiles) { return (tiles + sms - 1) / sms; };
   // token tiles: at most this many (an expert's last one may be ragged)
-  auto tiles = [&](int64_t tm) {
-    return p.offsets ? p.M / tm + (p.M < p.E ? p.M : p.E) : (p.M + tm - 1) / tm;
-  };
-  const int64_t tt = tiles(128);
+  const int64_t tt = p.offsets ? p.M / 128 + (p.M < p.E ? p.M : p.E) : (p.M + 127) / 128;
+  const int64_t u128 = tt * ((nw + 127) / 128), u256 = tt * ((nw + 255) / 256);
   const int64_t per = p.offsets ? (p.M + p.E - 1) / p.E : p.M;      // rows of an expert, on average
   p.box = per > 64 ? 128 : p.M <= 16 ? 16 : 32;
-  const int64_t nw = FUSED ? p.I : p.N, sms = num_sms();
-  static const int V = getenv("V") ? atoi(getenv("V")) : 0;
+  if (2 * u128 <= sms) return launch_fp4<FMT, 128, FUSED, false, true>(t, w, tt, p, stream);
   if constexpr (FUSED) {
-    if (V == 1) return launch_fp4<FMT, 64, true, false, true>(t, w, tt, p, stream);
-    if (V == 2) return launch_fp4<FMT, 128, true, false, false>(t, w, tt, p, stream);
-    if (V == 3) return launch_fp4<FMT, 128, true, true, false>(t, w, tiles(256), p, stream);
-    if (3 * tt * (nw / 128) < 2 * sms) return launch_fp4<FMT, 64, true, false, true>(t, w, tt, p, stream);
     return launch_fp4<FMT, 128, true, false, false>(t, w, tt, p, stream);
   } else {
-    if (V == 1) return launch_fp4<FMT, 128, false, false, true>(t, w, tt, p, stream);
-    if (V == 2) return launch_fp4<FMT, 128, false, false, false>(t, w, tt, p, stream);
-    if (V == 3) return launch_fp4<FMT, 256, false, true, false>(t, w, tiles(256), p, stream);
-    if (V == 4) return launch_fp4<FMT, 256, false, false, false>(t, w, tt, p, stream);
-    const int64_t u128 = tt * ((nw + 127) / 128), u256 = tt * ((nw + 255) / 256);
-    if (V == 9 || u128 <= sms / 2 || (u128 < sms && per <= 64)) return launch_fp4<FMT, 128, false, false, true>(t, w, tt, p, stream);
-    if (!p.offsets && tiles(256) * ((nw + 255) / 256) >= sms / 2 && p.M > 128)
-      return launch_fp4<FMT, 256, false, true, false>(t, w, tiles(256), p, stream);
-    if (2 * ((u256 + sms - 1) / sms) > (u128 + sms - 1) / sms) return launch_fp4<FMT, 128, false, false, false>(t, w, tt, p, stream);
+    const int64_t pairs = (p.M + 255) / 256 * ((nw + 255) / 256);
+    if (!p.offsets && p.M > 128 && 2 * pairs >= sms)
+      return launch_fp4<FMT, 256, false, true, false>(t, w, (p.M + 255) / 256, p, stream);
+    if (2 * rounds(u256) > rounds(u128)) return launch_fp4<FMT, 128, false, false, false>(t, w, tt, p, stream);
     return launch_fp4<FMT, 256, false, false, false>(t, w, tt, p, stream);
   }
 }

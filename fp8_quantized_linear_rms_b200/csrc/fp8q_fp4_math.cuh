@@ -97,6 +97,20 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float* y, const Fp4Scale& s
   return c;
 }
 
+// One value's code, in the low four bits.
+template <int FMT>
+__device__ __forceinline__ uint32_t fp4_code1(float y, const Fp4Scale& s) {
+  float v = y * s.rcp;
+  if constexpr (FMT == kNv) v = fminf(fabsf(fmaf(fmaf(-v, s.d, y), s.rcp, v)), 8.0f);
+  uint32_t c;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "mov.b32 %0, {b, 0, 0, 0};\n\t}"
+      : "=r"(c)
+      : "f"(copysignf(v, y)), "f"(0.0f));
+  return c;
+}
+
 // fp32 silu(g) u: e = 2^(-g log2 e) by ex2.approx of the rounded product plus
 // its exact residual (first order), one rounding of 1 + e, a division good to
 // 2 ulp and a product: relative error below 2^-20 for |g| <= 85.  Beyond, e over- or

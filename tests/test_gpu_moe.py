@@ -152,6 +152,7 @@ def rows_of(plan):
 def test_scattered_quant(fmt, T, k, E, K):
     ids, _ = routed(T, k, E, 1, 0.2)
     plan = fq.fp8q_moe_plan(ids, E)
+    torch.manual_seed(T + K)
     x = torch.randn(T, K + 8, device="cuda").to(torch.bfloat16)[:, :K]
     q, sf = fq.fp8q_moe_fp4_quant(x, plan, fmt)
     tok, _ = rows_of(plan)
@@ -171,6 +172,7 @@ CASES = [(1, 2, 4, 128, 64), (20, 2, 8, 272, 160), (130, 2, 2, 400, 256), (600, 
 def test_grouped_mm(fmt, T, k, E, N, K):
     ids, _ = routed(T, k, E, 2, 0.1)
     plan = fq.fp8q_moe_plan(ids, E)
+    torch.manual_seed(T + K)
     x = torch.randn(T, K, device="cuda").to(torch.bfloat16)
     q, sf = fq.fp8q_moe_fp4_quant(x, plan, fmt)
     w, wsf, wv = weights(E, N, K, fmt, 3)
@@ -193,9 +195,13 @@ def test_silu_quant_epilogue(fmt, T, k, E, I, K):
     """Codes and scales of the quantized hidden rows.  The kernel's y differs from the definition's
     by its fp32 accumulation and SiLU (below 2^-15 of the largest term; gate and up are sums whose
     own error the absolute products bound), so a code may differ by one step where the exact
-    quotient lies that near a rounding border, and a group is skipped where its scale does."""
+    quotient lies that near a rounding border, and a group is skipped where its scale does.  How many
+    that may be: the tolerance is about 2^-13 of a typical y, and a scale's borders lie 2^-3 to 2^-4
+    apart, a code's 2^-2: about 2e-3 of the groups and values.  They fall independently, so a count of
+    mean m stays below m + 5 sqrt(m) + 5 (Poisson, 1e-6)."""
     ids, _ = routed(T, k, E, 4, 0.1)
     plan = fq.fp8q_moe_plan(ids, E)
+    torch.manual_seed(T + K)
     x = torch.randn(T, K, device="cuda").to(torch.bfloat16)
     q, sf = fq.fp8q_moe_fp4_quant(x, plan, fmt)
     w, wsf, wv = weights(E, 2 * I, K, fmt, 5)
@@ -232,7 +238,8 @@ def test_silu_quant_epilogue(fmt, T, k, E, I, K):
         assert ok[wide].all()
         moved += int((got != fp4.quantize(y, fmt, g)[0])[wide].sum())
         total += int(wide.sum())
-    assert skipped <= 2e-3 * total / G + 2 and moved <= 2e-3 * total + 2
+    for n, of in ((skipped, total / G), (moved, total)):
+        assert n <= 2e-3 * of + 5 * (2e-3 * of) ** 0.5 + 5
 
 
 @pytest.mark.parametrize("T,k,H", [(1, 8, 64), (37, 6, 136), (1000, 9, 2048), (3, 32, 8)])
@@ -240,6 +247,7 @@ def test_combine(T, k, H):
     """A sum of k fp32 products (k 2^-24 of the absolute sum), rounded once to bf16 (2^-8)."""
     ids, w = routed(T, k, max(k, 40), 6, 0.2)
     plan = fq.fp8q_moe_plan(ids, max(k, 40))
+    torch.manual_seed(T + H)
     o = torch.randn(T * k, H + 8, device="cuda").to(torch.bfloat16)[:, :H]
     o[int(plan.offsets[-1]):] = float("nan")                           # rows without an expert
     y = fq.fp8q_moe_combine(o, plan, w)
@@ -265,6 +273,7 @@ def test_experts(fmt, T, k, E, H, I, absent):
     quantization of the hidden rows leaves open: a code that moves one step changes y by at most
     2^-2 of its term, and few do, so the whole is held in the norm."""
     ids, w = routed(T, k, E, 7, absent)
+    torch.manual_seed(T + H)
     x = torch.randn(T, H + 16, device="cuda").to(torch.bfloat16)[:, :H]
     w13, s13, v13 = weights(E, 2 * I, H, fmt, 8)
     w2, s2, v2 = weights(E, H, I, fmt, 9)
