@@ -19,7 +19,7 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 struct RouteParams {
   const void* logits;        // fp32 or bf16 [T, E], leading dimension ld
   int64_t T, ld;
-  int E, bf16, sigmoid;
+  int E, bf16, vec, sigmoid;  // vec: rows begin at 16-byte boundaries
   const float* bias;         // [E] or null
   int groups, topg, topk, renorm;
   float scale;
@@ -32,6 +32,46 @@ __device__ __forceinline__ float route_logit(const RouteParams& p, int64_t t, in
   const float v = p.bf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.logits) + t * p.ld + e)) << 16)
                          : __ldg(static_cast<const float*>(p.logits) + t * p.ld + e);
   return v != v ? -INFINITY : v + 0.0f;
+}
+
+// Bound of what the fp32 scores' errors make of the difference of two keys.  A
+// sigmoid: expf 2 ulp (2^-22), an addition and a division, below 2^-21 each.  A
+// softmax: the same and the rounded argument (d e^-d 2^-24), and the common
+// factor 1 / z, whose sum of at most 16 terms a lane and 5 levels is good to
+// 2^-19.2 of a difference of at most 1: together below 2^-18.  Twice that for
+// the sum of a group's two.  (The keys' own rounding is counted with them.)
+constexpr float kRouteError = 0x1p-17f;
+
+// A lane's V logits of token t: experts [V lane, V lane + V), -inf beyond E.
+template <int V, bool BF16>
+__device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int lane, float* l) {
+  constexpr int BYTES = V * (BF16 ? 2 : 4);
+  if constexpr (BYTES >= 8) {
+    // whole lanes, 8 or 16 bytes at a time, where rows allow it
+    constexpr int W = BYTES % 16 == 0 ? 16 : 8;
+    const uint8_t* row = static_cast<const uint8_t*>(p.logits) + (t * p.ld + V * lane) * (BF16 ? 2 : 4);
+    if (p.vec && V * lane + V <= p.E) {
+      uint32_t w[BYTES / 4];
+#pragma unroll
+      for (int i = 0; i < BYTES; i += W) {
+        if constexpr (W == 16) {
+          const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + i));
+          w[i / 4] = q.x, w[i / 4 + 1] = q.y, w[i / 4 + 2] = q.z, w[i / 4 + 3] = q.w;
+        } else {
+          const uint2 q = __ldg(reinterpret_cast<const uint2*>(row + i));
+          w[i / 4] = q.x, w[i / 4 + 1] = q.y;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float x = __uint_as_float(BF16 ? (v & 1 ? w[v / 2] & 0xFFFF0000u : w[v / 2] << 16) : w[v]);
+        l[v] = x != x ? -INFINITY : x + 0.0f;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) l[v] = V * lane + v < p.E ? route_logit(p, t, V * lane + v) : -INFINITY;
 }
 
 // Order-preserving integers of floating numbers; 0 is below all of them.
@@ -59,13 +99,117 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
   return (static_cast<uint64_t>(mh) << 32) | ml;
 }
 
-// One warp a token; lane holds experts lane, lane + 32, ... (V of them).  Key:
-// the 32-bit order of the logit where the selection has no bias (both scores
-// grow with the logit, so this is the exact order), else the 64-bit order of
-// score + bias in fp64: two biased scores that differ in exact arithmetic
-// differ there too, but for accidents below 2^-50.  Equal keys go to the
-// lowest expert.
-template <int V, typename Key>
+// The k largest keys of a token, one warp: lane holds experts [V lane, V lane +
+// V).  Groups first: a group counts with its largest key, or (TOP2) the sum of
+// its two largest; experts outside the best topg get key 0.  Equal keys go to
+// the lowest expert: the first lane's, and its first.  Returns lane j's j-th
+// expert.  32-bit keys of sums (TOP2) carry an error: `sure` is cleared where a
+// decision is closer than that.
+template <int V, typename Key, bool TOP2>
+__device__ __forceinline__ int route_select(const RouteParams& p, Key (&key)[V], int lane, bool& sure) {
+  constexpr bool ROUGH = TOP2 && sizeof(Key) == 4;
+  // a >= b are apart: |a - b| above the error of both
+  auto apart = [&](Key a, Key b) {
+    if constexpr (ROUGH) {
+      if (b <= order_key(-INFINITY)) return true;            // masked or excluded: exact
+      const float x = key_float(a), y = key_float(b);
+      return x - y > kRouteError + 0x1p-21f * (fabsf(x) + fabsf(y));
+    }
+    return true;
+  };
+  if (p.topg < p.groups) {
+    const int size = p.E / p.groups;
+    const bool whole = size % V == 0;   // a lane's experts lie in one group
+    Key t1 = 0, t2 = 0;
+    if (whole) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (key[v] > t1) { t2 = t1; t1 = key[v]; }
+        else if (key[v] > t2) t2 = key[v];
+      }
+    }
+    const int own = V * lane / size;
+    Key mine = 0;                       // lane g: group g's score
+    for (int g = 0; g < p.groups; ++g) {
+      Key a = 0, b = 0;                 // the lane's two largest of the group
+      if (whole) {
+        a = own == g ? t1 : 0;
+        b = own == g ? t2 : 0;
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int e = V * lane + v;
+          if (e >= g * size && e < (g + 1) * size) {
+            if (key[v] > a) { b = a; a = key[v]; }
+            else if (key[v] > b) b = key[v];
+          }
+        }
+      }
+      Key s = warp_max(a);
+      if constexpr (TOP2) {
+        if (size > 1) {
+          const int owner = __ffs(__ballot_sync(kAll, a == s)) - 1;
+          const Key second = warp_max(lane == owner ? b : a);
+          if constexpr (sizeof(Key) == 4) s = order_key(key_float(s) + key_float(second) + 0.0f);
+          else s = order_key(key_double(s) + key_double(second) + 0.0);
+        }
+      }
+      if (lane == g) mine = s;
+    }
+    uint32_t keep = 0;
+    Key last = 0;
+    for (int j = 0; j <= p.topg; ++j) {
+      const Key s = warp_max(mine);
+      if (j == p.topg) {                // the best group left out
+        sure = sure && apart(last, s);
+        break;
+      }
+      last = s;
+      const int g = __ffs(__ballot_sync(kAll, mine == s && lane < p.groups && !((keep >> lane) & 1u))) - 1;
+      keep |= 1u << g;
+      if (lane == g) mine = 0;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = V * lane + v;
+      if (e >= p.E || !((keep >> (whole ? own : e / size)) & 1u)) key[v] = 0;
+    }
+  }
+
+  int id = 0;
+  Key last = 0;
+  const int rounds = ROUGH ? p.topk + 1 : p.topk;
+  for (int j = 0; j < rounds; ++j) {
+    Key a = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) a = key[v] > a ? key[v] : a;
+    const Key best = warp_max(a);
+    if (ROUGH && j > 0) sure = sure && apart(last, best);
+    if (j == p.topk) break;
+    last = best;
+    int e = 0;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v)
+      if (key[v] == best) e = v;
+    const int owner = __ffs(__ballot_sync(kAll, a == best)) - 1;
+    if (lane == owner) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v == e) key[v] = 0;
+    }
+    e = __shfl_sync(kAll, V * lane + e, owner);
+    if (lane == j) id = e;
+  }
+  return id;
+}
+
+// One warp a token.  Without a bias both scores grow with the logit, so the
+// order of the logits is the exact one.  With a bias the selection is decided
+// by score + bias in fp32 where the keys are further apart than its error
+// (kRouteError, and their rounding), else again in fp64: there two biased
+// scores that differ in exact arithmetic differ too, but for accidents below
+// 2^-50.  (fp64 for every token took 42 us at 8192 tokens of 256 experts.)
+template <int V, bool BIASED, bool BF16>
 __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -73,20 +217,15 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   griddep_launch_dependents();
   if (t >= p.T) return;
 
-  constexpr bool BIASED = sizeof(Key) == 8;
   float l[V];
-  Key key[V];
+  load_logits<V, BF16>(p, t, lane, l);
   uint32_t top = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * 32 + lane;
-    l[v] = e < p.E ? route_logit(p, t, e) : -INFINITY;
-    if (e < p.E) top = max(top, order_key(l[v]));
-  }
+  for (int v = 0; v < V; ++v)
+    if (V * lane + v < p.E) top = max(top, order_key(l[v]));
   // softmax: the largest logit and the sum of exponentials (terms equal to the
   // maximum count 1, infinite ones too); no sum where every logit is masked
   float m = 0.0f, z = 1.0f;
-  double zd = 1.0;
   if (!p.sigmoid) {
     m = key_float(warp_max(top));
     z = 0.0f;
@@ -95,98 +234,62 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
       if (l[v] > -INFINITY) z += l[v] == m ? 1.0f : expf(l[v] - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
-    if constexpr (BIASED) {
-      zd = 0.0;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (l[v] > -INFINITY) zd += l[v] == m ? 1.0 : exp(static_cast<double>(l[v]) - static_cast<double>(m));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(kAll, zd, o);
-    }
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = v * 32 + lane;
-    key[v] = 0;
-    if (e < p.E) {
-      if constexpr (BIASED) {
-        double c = -INFINITY;
-        if (l[v] > -INFINITY) {
-          const double ld = l[v];
-          const double s = p.sigmoid ? 1.0 / (1.0 + exp(-ld))
-                                     : (l[v] == m ? 1.0 : exp(ld - static_cast<double>(m))) / zd;
-          c = s + static_cast<double>(__ldg(p.bias + e)) + 0.0;
-        }
-        key[v] = order_key(c);
-      } else {
-        key[v] = order_key(l[v]);
-      }
-    }
-  }
+  auto score = [&](float x) {
+    if (p.sigmoid) return 1.0f / (1.0f + expf(-x));
+    return x > -INFINITY ? (x == m ? 1.0f : expf(x - m)) / z : 0.0f;
+  };
 
-  // groups of neighbouring experts: a group's score is its largest key, or
-  // with a bias the sum of its two largest; experts outside the best topg
-  // groups get key 0
-  if (p.topg < p.groups) {
-    const int size = p.E / p.groups;
-    Key mine = 0;                       // lane g: group g's score
-    for (int g = 0; g < p.groups; ++g) {
-      Key a = 0, b = 0;                 // the lane's two largest of the group
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = v * 32 + lane;
-        if (e >= g * size && e < (g + 1) * size) {
-          if (key[v] > a) { b = a; a = key[v]; }
-          else if (key[v] > b) b = key[v];
-        }
-      }
-      Key s = warp_max(a);
-      if constexpr (BIASED) {
-        if (size > 1) {
-          const int owner = __ffs(__ballot_sync(kAll, a == s)) - 1;
-          const Key second = warp_max(lane == owner ? b : a);
-          s = order_key(key_double(s) + key_double(second) + 0.0);
-        }
-      }
-      if (lane == g) mine = s;
-    }
-    uint32_t keep = 0;
-    for (int j = 0; j < p.topg; ++j) {
-      const Key s = warp_max(mine);
-      const int g = __ffs(__ballot_sync(kAll, mine == s && lane < p.groups && !((keep >> lane) & 1u))) - 1;
-      keep |= 1u << g;
-      if (lane == g) mine = 0;
-    }
+  int id;
+  bool sure = true;
+  {
+    uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = v * 32 + lane;
-      if (e < p.E && !((keep >> (e / size)) & 1u)) key[v] = 0;
+      const int e = V * lane + v;
+      key[v] = 0;
+      if (e < p.E) {
+        float c = l[v];
+        if constexpr (BIASED) c = c > -INFINITY ? score(c) + __ldg(p.bias + e) + 0.0f : -INFINITY;
+        key[v] = order_key(c);
+      }
+    }
+    id = route_select<V, uint32_t, BIASED>(p, key, lane, sure);
+  }
+  if constexpr (BIASED) {
+    if (!sure) {
+      double zd = 1.0;
+      if (!p.sigmoid) {
+        zd = 0.0;
+#pragma unroll 1
+        for (int v = 0; v < V; ++v) {
+          const float x = V * lane + v < p.E ? route_logit(p, t, V * lane + v) : -INFINITY;
+          if (x > -INFINITY) zd += x == m ? 1.0 : exp(static_cast<double>(x) - static_cast<double>(m));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(kAll, zd, o);
+      }
+      uint64_t key[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = V * lane + v;
+        key[v] = 0;
+        if (e < p.E) {
+          double c = -INFINITY;
+          if (l[v] > -INFINITY) {
+            const double x = l[v];
+            const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x))
+                                       : (l[v] == m ? 1.0 : exp(x - static_cast<double>(m))) / zd;
+            c = s + static_cast<double>(__ldg(p.bias + e)) + 0.0;
+          }
+          key[v] = order_key(c);
+        }
+      }
+      id = route_select<V, uint64_t, true>(p, key, lane, sure);
     }
   }
 
-  int id = 0;                           // lane j: the j-th expert
-  for (int j = 0; j < p.topk; ++j) {
-    Key a = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) a = key[v] > a ? key[v] : a;
-    const Key best = warp_max(a);
-    uint32_t e = 0xFFFFFFFFu;           // the lane's first expert with it
-#pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] == best) e = v * 32 + lane;
-    e = __reduce_min_sync(kAll, e);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (e == static_cast<uint32_t>(v * 32 + lane)) key[v] = 0;
-    if (lane == j) id = static_cast<int>(e);
-  }
-
-  float s = 0.0f;
-  if (lane < p.topk) {
-    const float x = route_logit(p, t, id);
-    if (p.sigmoid) s = 1.0f / (1.0f + expf(-x));
-    else if (x > -INFINITY) s = (x == m ? 1.0f : expf(x - m)) / z;
-  }
+  float s = lane < p.topk ? score(route_logit(p, t, id)) : 0.0f;
   if (p.renorm) {
     float sum = s;
 #pragma unroll
@@ -203,7 +306,9 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
 // A stable counting sort of n (token, slot) entries by expert, in entry order
 // within an expert, without atomics on results: every count and rank comes
 // from a fixed order.  A block takes up to kPlanBlock entries, a warp a
-// contiguous part of them; __match_any_sync gives the ranks inside 32 entries.
+// contiguous part of them; a ballot for each bit of the expert gives the ranks
+// inside 32 entries (__match_any_sync, whose cost grows with the number of
+// distinct values, took 17 us for 32768 entries of 128 experts).
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanBlock = 4096;
@@ -211,6 +316,7 @@ constexpr int kPlanBlock = 4096;
 struct PlanParams {
   const int* ids;
   int n, E, blocks;
+  int bits;          // that tell E experts and none (all ones) apart
   int* offsets;      // [E + 1]
   int* sf_offsets;   // [E + 1]
   int* pos;          // [n]
@@ -218,67 +324,124 @@ struct PlanParams {
   int* hist;         // [blocks, E] counts of the blocks (blocks > 1)
 };
 
-// Counts of the warp's entries [i0, i1) into cnt[E] (shared, the warp's own).
-__device__ __forceinline__ void warp_count(const PlanParams& p, int i0, int i1, int* cnt, int lane) {
-  for (int i = i0; i < i1; i += 32) {
-    const int e = i + lane < i1 ? __ldg(p.ids + i + lane) : -1;
-    const bool in = e >= 0 && e < p.E;
-    const unsigned same = __match_any_sync(kAll, in ? e : -1);
-    if (in && lane == __ffs(same) - 1) cnt[e] += __popc(same);
+// A warp's part of a block: kPlanSteps steps of 32 entries, read at once (a
+// load a step would wait out the latency of each).  Absent or foreign experts
+// become -1.
+constexpr int kPlanSteps = kPlanBlock / kPlanWarps / 32;
+
+__device__ __forceinline__ void plan_load(const PlanParams& p, int i0, int lane, int* e) {
+#pragma unroll
+  for (int k = 0; k < kPlanSteps; ++k) {
+    const int i = i0 + 32 * k + lane;
+    e[k] = i < p.n ? __ldg(p.ids + i) : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < kPlanSteps; ++k)
+    if (e[k] >= p.E) e[k] = -1;
+}
+
+// Lanes of the warp with the same value of the low `bits` bits.
+__device__ __forceinline__ unsigned same_lanes(int e, int bits) {
+  unsigned m = kAll;
+  for (int b = 0; b < bits; ++b) {
+    const bool set = (e >> b) & 1;
+    const unsigned v = __ballot_sync(kAll, set);
+    m &= set ? v : ~v;
+  }
+  return m;
+}
+
+// Counts of the warp's entries into cnt[E] (shared, the warp's own).
+__device__ __forceinline__ void warp_count(const int* e, int steps, int bits, int* cnt, int lane) {
+#pragma unroll
+  for (int k = 0; k < kPlanSteps; ++k) {
+    if (k >= steps) break;
+    const unsigned same = same_lanes(e[k], bits);
+    if (e[k] >= 0 && lane == __ffs(same) - 1) cnt[e[k]] += __popc(same);
     __syncwarp();
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_count_kernel(const PlanParams p) {
-  extern __shared__ int cnt[];                          // [warps][E]
+  extern __shared__ int cnt[];                          // [warps][E + 1]: no two of 32 neighbours in a bank
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kPlanWarps * p.E; i += kPlanThreads) cnt[i] = 0;
+  for (int i = threadIdx.x; i < kPlanWarps * (p.E + 1); i += kPlanThreads) cnt[i] = 0;
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  const int part = kPlanBlock / kPlanWarps;
-  const int i0 = blockIdx.x * kPlanBlock + warp * part;
-  warp_count(p, i0, min(p.n, i0 + part), cnt + warp * p.E, lane);
+  const int i0 = static_cast<int>(blockIdx.x) * kPlanBlock + warp * 32 * kPlanSteps;
+  const int steps = (p.n - i0 + 31) >> 5;               // with entries; none where negative
+  int id[kPlanSteps];
+  plan_load(p, i0, lane, id);
+  warp_count(id, steps, p.bits, cnt + warp * (p.E + 1), lane);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
+  // eight lanes an expert, four warps' counts each
+  const int sub = threadIdx.x & 7;
+  for (int e0 = 0; e0 < p.E; e0 += kPlanThreads / 8) {
+    const int e = e0 + (threadIdx.x >> 3);
     int s = 0;
-    for (int w = 0; w < kPlanWarps; ++w) s += cnt[w * p.E + e];
-    p.hist[blockIdx.x * p.E + e] = s;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps / 8; ++w) s += e < p.E ? cnt[(sub * (kPlanWarps / 8) + w) * (p.E + 1) + e] : 0;
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) s += __shfl_xor_sync(kAll, s, o);
+    if (sub == 0 && e < p.E) p.hist[blockIdx.x * p.E + e] = s;
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanParams p) {
-  extern __shared__ int cnt[];                          // [warps][E]: counts, then first ranks of the warps
+  extern __shared__ int cnt[];                          // [warps][E + 1]: counts, then first ranks of the warps
   __shared__ int first[kMaxExperts + 1], sf_first[kMaxExperts + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = threadIdx.x; i < kPlanWarps * p.E; i += kPlanThreads) cnt[i] = 0;
+  for (int i = threadIdx.x; i < kPlanWarps * (p.E + 1); i += kPlanThreads) cnt[i] = 0;
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  // one block: parts of whole 32-entry steps spread over the warps
-  const int per = p.blocks > 1 ? kPlanBlock : (p.n + kPlanWarps * 32 - 1) / (kPlanWarps * 32) * (kPlanWarps * 32);
-  const int part = per / kPlanWarps;
-  const int i0 = min(p.n, static_cast<int>(blockIdx.x) * per + warp * part);
-  const int i1 = min(p.n, i0 + part);
-  warp_count(p, i0, i1, cnt + warp * p.E, lane);
+  const int i0 = static_cast<int>(blockIdx.x) * kPlanBlock + warp * 32 * kPlanSteps;
+  const int steps = (p.n - i0 + 31) >> 5;               // with entries; none where negative
+  int id[kPlanSteps];
+  plan_load(p, i0, lane, id);
+  warp_count(id, steps, p.bits, cnt + warp * (p.E + 1), lane);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kPlanThreads) {
-    // the expert's entries in the blocks before this one, in all, and before each warp
+  // Eight lanes an expert: its entries in the blocks before this one and in
+  // all (each lane every eighth block), and before each warp (four warps each).
+  const int sub = threadIdx.x & 7;
+  for (int e0 = 0; e0 < p.E; e0 += kPlanThreads / 8) {
+    const int e = e0 + (threadIdx.x >> 3);
+    const bool in = e < p.E;
     int before = 0, total = 0;
-    if (p.blocks > 1) {
-      for (int b = 0; b < p.blocks; ++b) {
-        const int c = p.hist[b * p.E + e];
+    if (p.blocks > 1 && in) {
+      for (int b = sub; b < p.blocks; b += 8) {
+        const int c = __ldg(p.hist + b * p.E + e);
         if (b < static_cast<int>(blockIdx.x)) before += c;
         total += c;
       }
     }
-    int run = before;
-    for (int w = 0; w < kPlanWarps; ++w) {
-      const int c = cnt[w * p.E + e];
-      cnt[w * p.E + e] = run;
-      run += c;
+    int c[kPlanWarps / 8], mine = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps / 8; ++w) {
+      c[w] = in ? cnt[(sub * (kPlanWarps / 8) + w) * (p.E + 1) + e] : 0;
+      mine += c[w];
     }
-    first[e + 1] = p.blocks > 1 ? total : run;
+    int run = mine;                                     // inclusive over the lanes
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const int v = __shfl_up_sync(kAll, run, o, 8);
+      if (sub >= o) run += v;
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      before += __shfl_xor_sync(kAll, before, o);
+      total += __shfl_xor_sync(kAll, total, o);
+    }
+    if (in) {
+      if (sub == 7) first[e + 1] = p.blocks > 1 ? total : run;
+      int at = before + run - mine;
+#pragma unroll
+      for (int w = 0; w < kPlanWarps / 8; ++w) {
+        cnt[(sub * (kPlanWarps / 8) + w) * (p.E + 1) + e] = at;
+        at += c[w];
+      }
+    }
   }
   __syncthreads();
   if (warp == 0) {                                      // sums over experts
@@ -306,19 +469,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_place_kernel(const PlanPara
       p.offsets[e] = first[e];
       p.sf_offsets[e] = sf_first[e];
     }
-  int* mine = cnt + warp * p.E;
-  for (int i = i0; i < i1; i += 32) {
-    const bool live = i + lane < i1;
-    const int e = live ? __ldg(p.ids + i + lane) : -1;
-    const bool in = e >= 0 && e < p.E;
-    const unsigned same = __match_any_sync(kAll, in ? e : -1);
-    const int rank = in ? mine[e] + __popc(same & ((1u << lane) - 1u)) : 0;
+  int* mine = cnt + warp * (p.E + 1);
+#pragma unroll
+  for (int k = 0; k < kPlanSteps; ++k) {
+    if (k >= steps) break;
+    const int i = i0 + 32 * k + lane, e = id[k];
+    const unsigned same = same_lanes(e, p.bits);
+    const int rank = e >= 0 ? mine[e] + __popc(same & ((1u << lane) - 1u)) : 0;
     __syncwarp();
-    if (in && lane == __ffs(same) - 1) mine[e] += __popc(same);
+    if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
     __syncwarp();
-    if (live) {
-      p.pos[i + lane] = in ? first[e] + rank : -1;
-      p.sf_row[i + lane] = in ? sf_first[e] * 128 + rank : -1;
+    if (i < p.n) {
+      p.pos[i] = e >= 0 ? first[e] + rank : -1;
+      p.sf_row[i] = e >= 0 ? sf_first[e] * 128 + rank : -1;
     }
   }
 }
@@ -363,14 +526,20 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* o, int64_t
   }
 }
 
-template <typename Key>
-fp8q_status launch_route(const RouteParams& p, cudaStream_t s) {
+template <int V>
+fp8q_status launch_route_v(const RouteParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((p.T + 7) / 8)), block(p.T < 8 ? 32 * static_cast<unsigned>(p.T) : 256);
-  if (p.E <= 32) return launch_kernel(route_kernel<1, Key>, grid, block, 0, s, 1, p);
-  if (p.E <= 64) return launch_kernel(route_kernel<2, Key>, grid, block, 0, s, 1, p);
-  if (p.E <= 128) return launch_kernel(route_kernel<4, Key>, grid, block, 0, s, 1, p);
-  if (p.E <= 256) return launch_kernel(route_kernel<8, Key>, grid, block, 0, s, 1, p);
-  return launch_kernel(route_kernel<16, Key>, grid, block, 0, s, 1, p);
+  auto kern = p.bias ? (p.bf16 ? route_kernel<V, true, true> : route_kernel<V, true, false>)
+                     : (p.bf16 ? route_kernel<V, false, true> : route_kernel<V, false, false>);
+  return launch_kernel(kern, grid, block, 0, s, 1, p);
+}
+
+fp8q_status launch_route(const RouteParams& p, cudaStream_t s) {
+  if (p.E <= 32) return launch_route_v<1>(p, s);
+  if (p.E <= 64) return launch_route_v<2>(p, s);
+  if (p.E <= 128) return launch_route_v<4>(p, s);
+  if (p.E <= 256) return launch_route_v<8>(p, s);
+  return launch_route_v<16>(p, s);
 }
 
 int64_t plan_blocks(int64_t n) { return n <= kPlanBlock ? 1 : (n + kPlanBlock - 1) / kPlanBlock; }
@@ -427,10 +596,10 @@ extern "C" fp8q_status fp8q_moe_route(const void* logits, int logits_bf16, int64
   if (!logits || !weights || !ids) return FP8Q_ERR_INVALID_ARG;
   if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(ids, 4))
     return FP8Q_ERR_INVALID_ARG;
-  const RouteParams p{logits, T, ldl, static_cast<int>(E), logits_bf16, scoring == FP8Q_ROUTE_SIGMOID, bias, num_groups,
-                      topk_groups, topk, renormalize, scale, weights, ids};
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return bias ? launch_route<uint64_t>(p, s) : launch_route<uint32_t>(p, s);
+  const int vec = aligned(logits, 16) && ldl * (logits_bf16 ? 2 : 4) % 16 == 0;
+  const RouteParams p{logits, T, ldl, static_cast<int>(E), logits_bf16, vec, scoring == FP8Q_ROUTE_SIGMOID, bias,
+                      num_groups, topk_groups, topk, renormalize, scale, weights, ids};
+  return launch_route(p, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" size_t fp8q_moe_plan_workspace_bytes(int64_t n, int64_t E) {
@@ -449,16 +618,18 @@ extern "C" fp8q_status fp8q_moe_plan(const int* ids, int64_t n, int64_t E, int* 
   const size_t need = fp8q_moe_plan_workspace_bytes(n, E);
   if (need > 0 && (!workspace || ws_bytes < need || !aligned(workspace, 4))) return FP8Q_ERR_INVALID_ARG;
   const int blocks = static_cast<int>(n > 0 ? plan_blocks(n) : 1);
-  const PlanParams p{ids, static_cast<int>(n), static_cast<int>(E), blocks, offsets, sf_offsets, pos, sf_row,
+  int bits = 1;
+  while ((1 << bits) <= E) ++bits;
+  const PlanParams p{ids, static_cast<int>(n), static_cast<int>(E), blocks, bits, offsets, sf_offsets, pos, sf_row,
                      static_cast<int*>(workspace)};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const size_t smem = static_cast<size_t>(kPlanWarps) * static_cast<size_t>(E) * 4;   // at most 64 KB
+  const size_t smem = static_cast<size_t>(kPlanWarps) * static_cast<size_t>(E + 1) * 4;   // at most 65 KB
   static std::atomic<int> attr_done[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8Q_ERR_CUDA;
   if (!attr_done[dev].load(std::memory_order_relaxed)) {
     for (auto k : {plan_count_kernel, plan_place_kernel})
-      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanWarps * kMaxExperts * 4) != cudaSuccess)
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanWarps * (kMaxExperts + 1) * 4) != cudaSuccess)
         return FP8Q_ERR_CUDA;
     attr_done[dev].store(1, std::memory_order_relaxed);
   }
