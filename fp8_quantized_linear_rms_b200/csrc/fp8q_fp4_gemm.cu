@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
 
   // SPLIT: the tile, and the factors that its output takes, before the long wait
   Fp4Tile tile0{};
-  const float gh = FUSED && p.gh ? *p.gh : 1.0f;
+  const Fp4G gh = fp4_g(FUSED ? p.gh : nullptr);
   const float ga = p.ga ? *p.ga : 1.0f;
   float gb = 1.0f;
   if (SPLIT && cta < units) {

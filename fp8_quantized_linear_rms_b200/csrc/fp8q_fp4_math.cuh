@@ -45,15 +45,32 @@ struct Fp4Scale {
   float d, rcp;
 };
 
-// g, and 1/6 of an amax, enter as IEEE quotients (__fdiv_rn).
+// A tensor scale and its correctly rounded reciprocal.
+struct Fp4G {
+  float g, rcp;
+};
+__device__ __forceinline__ Fp4G fp4_g(const float* g) {
+  const float v = g ? *g : 1.0f;
+  return {v, __frcp_rn(v)};
+}
+
+// nvfp4: both quotients by Markstein's correction step, as in fp4_codes8 (1/6
+// is rounded to nearest, too).  Its argument fails where a product under- or
+// overflows: a tiny quotient becomes scale 0 either way, and of an infinite
+// amax or quotient the minima make the largest scale (a NaN is dropped).
 template <int FMT>
-__device__ __forceinline__ Fp4Scale fp4_scale(float amax, float g) {
+__device__ __forceinline__ Fp4Scale fp4_scale(float amax, const Fp4G& g) {
   Fp4Scale s;
   if constexpr (FMT == kNv) {
-    const float u = __fdiv_rn(__fdiv_rn(amax, 6.0f), g);
-    s.byte = static_cast<uint32_t>(__nv_cvt_float_to_fp8(u, __NV_SATFINITE, __NV_E4M3));
+    constexpr float kSixth = 1.0f / 6.0f;
+    const float a = fminf(amax, 3.40282347e38f);
+    float u = a * kSixth;
+    u = fmaf(fmaf(-6.0f, u, a), kSixth, u);
+    float q = u * g.rcp;
+    q = fminf(fmaf(fmaf(-g.g, q, u), g.rcp, q), 448.0f);
+    s.byte = static_cast<uint32_t>(__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3));
     const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(s.byte), __NV_E4M3);
-    s.d = __fmul_rn(__half2float(__half(h)), g);
+    s.d = __fmul_rn(__half2float(__half(h)), g.g);
     s.rcp = s.d > 0.0f ? __frcp_rn(s.d) : 0.0f;
   } else {
     // fl32(max(amax, 1e-10) / 6) >= 2^-36 is a positive normal; its exponent,
@@ -74,8 +91,10 @@ __device__ __forceinline__ Fp4Scale fp4_scale(float amax, float g) {
 // residual y - q0 d exact under FMA, RN(q0 + r rcp) = RN(y / d) for
 // rcp = RN(1/d)); a quotient too small for that argument rounds to code 0
 // either way.  mxfp4: rcp is a power of two, the product is the quotient.
-// The copied sign keeps -0; the minimum, which drops a NaN, gives an infinite
-// y (whose residual is NaN) the saturated code.
+// The copied sign keeps -0; the minimum, which drops a NaN, gives an infinite y
+// (whose residual is NaN) the saturated code.
+// (Pairs of fp32 operations, .f32x2, were no faster: they cost the moves that
+// pair the registers.)
 template <int FMT>
 __device__ __forceinline__ uint32_t fp4_codes8(const float* y, const Fp4Scale& s) {
   float q[8];

@@ -55,15 +55,35 @@ __device__ __forceinline__ Item ld_item(const uint16_t* p, bool wide) {
   return v;
 }
 
-__device__ __forceinline__ uint4 silu_chunk(const uint4& g, const uint4& u) {
-  uint32_t d = 0;
-  bool bad = false;
-  uint4 y;
-  y.x = silu_pair(g.x, u.x, d, bad);
-  y.y = silu_pair(g.y, u.y, d, bad);
-  y.z = silu_pair(g.z, u.z, d, bad);
-  y.w = silu_pair(g.w, u.w, d, bad);
-  return (d | bad) ? silu_chunk_fix(g, u, y) : y;
+// Both ends of the bracket of bf16(silu(g) u) (the bounds of silu_pair): lo and
+// hi, bf16, |lo| <= |y| <= |hi|.  Chunks that the bracket does not serve (tiny
+// values or gates, gates below -85: tested on the packed bf16 words) are exact
+// at once.
+__device__ __forceinline__ uint32_t min_abs2(uint32_t m, uint32_t w) {
+  w &= 0x7FFF7FFFu;
+  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&w));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint4 silu_chunk(const uint4& g, const uint4& u, uint4& hi) {
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+  uint32_t lo[4], h[4], least = 0x7F807F80u;        // smallest magnitude of gates and lower ends
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t p = silu_p2(bf2_to_f2(gw[k]), bf2_to_f2(uw[k]));
+    lo[k] = f2_to_bf2_rn(mul2(p, dup2(kSiluLo)));
+    h[k] = f2_to_bf2_rn(mul2(p, dup2(kSiluHi)));
+    least = min_abs2(min_abs2(least, gw[k]), lo[k]);
+  }
+  uint4 y = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  // 2^-99: a lower end of at least that comes from a p above 2^-100
+  if (fminf(bf16_bits_to_f32(least & 0xFFFFu), bf16_bits_to_f32(least >> 16)) < 0x1p-99f || chunk_min_gate(g) < -85.0f)
+    hi = y = silu_chunk_fix(g, u, y);
+  return y;
+}
+
+__device__ __forceinline__ bool differ(const uint4& a, const uint4& b) {
+  return ((a.x ^ b.x) | (a.y ^ b.y) | (a.z ^ b.z) | (a.w ^ b.w)) != 0;
 }
 
 __device__ __forceinline__ void chunk_to_f32(const uint4& c, float* f) {
@@ -78,7 +98,7 @@ __device__ __forceinline__ void chunk_to_f32(const uint4& c, float* f) {
 // Codes and scale of one item, y already bf16.  mxfp4: every lane of a pair
 // must call it (shuffle); a lane without an item passes zeros.
 template <int FMT>
-__device__ __forceinline__ uint2 item_codes(const Item& y, float g, uint32_t* byte) {
+__device__ __forceinline__ uint2 item_codes(const Item& y, const Fp4G& g, uint32_t* byte) {
   float amax = absmax2_to_f32(chunk_absmax2(y.b, chunk_absmax2(y.a, 0u)));
   if constexpr (FMT == kMx) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
   const Fp4Scale s = fp4_scale<FMT>(amax, g);
@@ -118,35 +138,70 @@ __device__ __forceinline__ void emit_item(const Fp4QuantParams& p, int64_t row, 
   }
 }
 
-// Plain and SiLU*mul: independent items, one a thread and step.
+// Row of item i of `total`; a 32-bit division where it serves.
+__device__ __forceinline__ int64_t item_row(int64_t i, int items, int64_t total) {
+  return total <= 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(items)) : i / items;
+}
+
+// Plain and SiLU*mul: independent items, one a thread and step.  A warp takes 32
+// neighbouring items: their scale bytes lie in 8 blocks, a sector each.  (Eight
+// rows by four items instead, whose scales fill one sector, were slower: 70
+// against 65 us for 8192 x 12288 plain values.)
 constexpr int kItemThreads = 256;
 
 template <int FMT, int OP>
-__global__ void __launch_bounds__(kItemThreads) fp4_items_kernel(const Fp4QuantParams p, int wide) {
+__global__ void __launch_bounds__(kItemThreads, OP == OP_SILU ? 4 : 6) fp4_items_kernel(const Fp4QuantParams p, int wide) {
   const int items = static_cast<int>(p.K >> 4);
   const int64_t total = p.M * items;
   griddep_wait();
   griddep_launch_dependents();
-  const float g = p.g ? *p.g : 1.0f;
+  const Fp4G g = fp4_g(p.g);
+  const int lane = threadIdx.x & 31;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kItemThreads;
   // whole warps stay in the loop: total is even, so pairs of lanes live and end together
   for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kItemThreads + (threadIdx.x & ~31); i0 < total; i0 += stride) {
-    const int64_t i = i0 + (threadIdx.x & 31);
+    const int64_t i = i0 + lane;
     const bool live = i < total;
-    const int64_t row = live ? (total <= 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(items)) : i / items) : 0;
+    const int64_t row = live ? item_row(i, items, total) : 0;
     const int it = live ? static_cast<int>(i - row * items) : 0;
-    Item y = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (live) {
-      const uint16_t* x = p.x + row * p.ldx + 16 * it;
-      y = ld_item(x, wide);
-      if constexpr (OP == OP_SILU) {
-        const Item u = ld_item(x + p.K, wide);
-        y.a = silu_chunk(y.a, u.a);
-        y.b = silu_chunk(y.b, u.b);
-      }
-    }
+    const Item zero = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    Item y = zero;
     uint32_t byte;
-    const uint2 c = item_codes<FMT>(y, g, &byte);
+    uint2 c;
+    if constexpr (OP == OP_SILU) {
+      // Where the two ends of a value's bracket give the same codes and scale,
+      // so does the value between them (both are monotone): the exact value,
+      // an fp64 chain of some thousand cycles, is needed only where they do not
+      // (one in ~50 of the open brackets, themselves 5e-4 of the values).  What
+      // bounds the kernel is its instructions, ~40 a value (8192 x 12288 nvfp4:
+      // 153 us, 46% of HBM).  Tried and slower: a wider and cheaper bracket,
+      // whose ends are both coded for every value (169 us); three or five CTAs
+      // an SM (167, 152 with spills).
+      Item hi = zero;
+      const uint16_t* x = p.x + row * p.ldx + 16 * it;
+      if (live) {
+        const Item gate = ld_item(x, wide), up = ld_item(x + p.K, wide);
+        y.a = silu_chunk(gate.a, up.a, hi.a);
+        y.b = silu_chunk(gate.b, up.b, hi.b);
+      }
+      c = item_codes<FMT>(y, g, &byte);
+      const bool open = differ(y.a, hi.a) || differ(y.b, hi.b);
+      if (__any_sync(0xFFFFFFFFu, open)) {
+        uint32_t byte2;
+        const uint2 c2 = item_codes<FMT>(hi, g, &byte2);
+        if (__any_sync(0xFFFFFFFFu, byte != byte2 || c.x != c2.x || c.y != c2.y)) {
+          if (open) {                   // its inputs again, rather than in registers all along
+            const Item gate = ld_item(x, wide), up = ld_item(x + p.K, wide);
+            y.a = silu_chunk_fix(gate.a, up.a, y.a);
+            y.b = silu_chunk_fix(gate.b, up.b, y.b);
+          }
+          c = item_codes<FMT>(y, g, &byte);
+        }
+      }
+    } else {
+      if (live) y = ld_item(p.x + row * p.ldx + 16 * it, wide);
+      c = item_codes<FMT>(y, g, &byte);
+    }
     if (live) emit_item<FMT>(p, row, it, items, c, byte);
   }
 }
@@ -155,14 +210,14 @@ __global__ void __launch_bounds__(kItemThreads) fp4_items_kernel(const Fp4QuantP
 // the sum of squares in fp64.  IT items a thread stay in registers between the
 // two passes; IT = 0 (rows of any length) reads them again.
 template <int FMT, int IT>
-__global__ void __launch_bounds__(512) fp4_rms_kernel(const Fp4QuantParams p, int wide) {
+__global__ void __launch_bounds__(512, IT == 4 ? 1 : 2) fp4_rms_kernel(const Fp4QuantParams p, int wide) {
   __shared__ double red[32];
   const int items = static_cast<int>(p.K >> 4);
   const int T = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Item zero = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
   griddep_wait();
   griddep_launch_dependents();
-  const float g = p.g ? *p.g : 1.0f;
+  const Fp4G g = fp4_g(p.g);
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
     const uint16_t* x = p.x + row * p.ldx;
     Item v[IT ? IT : 1];
@@ -232,7 +287,7 @@ __global__ void __launch_bounds__(kItemThreads)
   const float g = gp ? *gp : 1.0f;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kItemThreads + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x) * kItemThreads) {
-    const int64_t row = total <= 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(items)) : i / items;
+    const int64_t row = item_row(i, items, total);
     const int it = static_cast<int>(i - row * items);
     const uint2 c = *reinterpret_cast<const uint2*>(q + row * ldq + 8 * it);
     const uint32_t b = sf[fp4_sf_offset(row, FMT == kNv ? it : it >> 1, kb)];
@@ -284,8 +339,10 @@ template <int FMT>
 fp8q_status launch_rms(const Fp4QuantParams& p, cudaStream_t stream) {
   const int wide = aligned(p.x, 32) && p.ldx % 16 == 0;
   const int64_t items = p.K >> 4;
-  // threads: whole warps, at most 512; items a thread as few as that allows
-  const int it = items <= 512 ? 1 : items <= 1024 ? 2 : items <= 2048 ? 4 : 0;
+  // Few rows: an item a thread, for the shortest row.  Many: two, and four
+  // where that takes over 512 threads, in short CTAs, so that many rows are in
+  // flight on an SM and cover each other's reductions.
+  const int it = items <= 512 && p.M <= 4 * num_sms() ? 1 : items <= 1024 ? 2 : items <= 2048 ? 4 : 0;
   const int64_t need = it ? (items + it - 1) / it : 512;
   const int T = static_cast<int>((need + 31) / 32 * 32);
   const int64_t cap = static_cast<int64_t>(num_sms()) * (2048 / T) * 4;
