@@ -897,7 +897,7 @@ def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
     """The experts' pass over tokens x bf16 [T, H]: y[t] = sum_j weights[t, j] W2_e quant(silu(gate) up),
     e = ids[t, j].  w13 codes [E, 2I, H/2] = [gate | up], w2 codes [E, H, I/2], with scale blocks
     [E, *fp4_sf_shape(rows, cols, fmt)]; x_gscale, h_gscale fp32 [1], w13_gscale, w2_gscale fp32 [E].
-    Six launches at most; ids outside [0, E) add nothing."""
+    Four launches for up to 128 (token, slot) entries, six at most; ids outside [0, E) add nothing."""
     _need(x, torch.bfloat16, "x")
     ldx = _rowmajor(x, "x")
     _need_codes(w13, "w13", 3)
@@ -919,6 +919,8 @@ def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
         workspace = _empty((n,), torch.uint8, x, stream)
     else:
         _need(workspace, torch.uint8, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
     st = lib.fp8q_moe_experts_fp4(
         x.data_ptr(), T, ldx, ids.data_ptr(), weights.data_ptr(), k, E, H, I, f, w13.data_ptr(), s13, w2.data_ptr(),
         s2, gx, g13, gh, g2, y.data_ptr(), ldy, workspace.data_ptr(), workspace.numel(),

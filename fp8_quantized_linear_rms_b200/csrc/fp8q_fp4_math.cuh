@@ -17,6 +17,15 @@
 #include "fp8q_fp4.h"
 
 namespace fp8q {
+
+// The plan of up to kSmallPlan (token, slot) entries and the quantization of
+// their tokens into the experts' rows, in one launch (arguments checked by the
+// caller; E <= 512).
+constexpr int kSmallPlan = 128;
+fp8q_status moe_plan_quant_small(const void* x, int64_t T, int64_t H, int64_t ldx, const int* ids, int topk, int E,
+                                 int format, const float* gscale, int* offsets, int* sf_offsets, int* pos, int* sf_row,
+                                 void* q, uint8_t* sf, cudaStream_t stream);
+
 namespace {   // internal linkage in every translation unit that includes it
 
 constexpr int kNv = FP8Q_FP4_NV, kMx = FP8Q_FP4_MX;

@@ -318,6 +318,72 @@ __global__ void __launch_bounds__(kItemThreads)
   }
 }
 
+// ------------------------------------------------- few tokens of experts' rows
+// Plan and quantization together, a CTA a token: with at most kSmallPlan
+// entries every CTA counts them all itself.  An expert then has at most one
+// block row of scales, so an entry's scales lie in the block row that counts
+// the experts present before its own.  Two launches took 5.6 us for a token.
+template <int FMT>
+__global__ void __launch_bounds__(kItemThreads)
+    moe_small_kernel(Fp4QuantParams p, const int* ids, int E, int* offsets, int* sf_offsets, int* pos, int* sf_row,
+                     int wide) {
+  __shared__ int id[kSmallPlan], row_of[kSmallPlan], srow_of[kSmallPlan];
+  __shared__ uint32_t present[16];                      // a bit for each expert with entries
+  const int n = static_cast<int>(p.M) * p.topk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid < 16) present[tid] = 0;
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  const Fp4G g = fp4_g(p.g);
+  if (tid < n) {
+    int e = __ldg(ids + tid);
+    if (e < 0 || e >= E) e = -1;
+    id[tid] = e;
+    if (e >= 0) atomicOr(&present[e >> 5], 1u << (e & 31));
+  }
+  __syncthreads();
+  // entries of experts before e, and of e before entry `upto`
+  auto below = [&](int e, int upto) {
+    int c = 0;
+    for (int i = 0; i < n; ++i) c += (id[i] >= 0 && id[i] < e) || (id[i] == e && i < upto);
+    return c;
+  };
+  auto blocks_below = [&](int e) {
+    int c = 0;
+    for (int w = 0; w <= (e - 1) >> 5; ++w) c += __popc(w == e >> 5 ? present[w] & ((1u << (e & 31)) - 1u) : present[w]);
+    return c;
+  };
+  const int64_t t = blockIdx.x;
+  if (warp == 0) {
+    for (int j = lane; j < p.topk; j += 32) {
+      const int i = static_cast<int>(t) * p.topk + j, e = id[i];
+      row_of[j] = e >= 0 ? below(e, i) : -1;
+      // the rank within the expert: rows before it less those of experts before
+      srow_of[j] = e >= 0 ? 128 * blocks_below(e) + row_of[j] - below(e, 0) : -1;
+      pos[i] = row_of[j];
+      sf_row[i] = srow_of[j];
+    }
+  } else if (t == 0) {
+    for (int e = tid - 32; e <= E; e += kItemThreads - 32) {
+      offsets[e] = below(e, 0);
+      sf_offsets[e] = blocks_below(e);
+    }
+  }
+  __syncthreads();
+  const int items = static_cast<int>(p.K >> 4);
+  const Item zero = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  for (int i0 = tid & ~31; i0 < items; i0 += kItemThreads) {
+    const int it = i0 + lane;
+    const bool live = it < items;
+    const Item y = live ? ld_item(p.x + t * p.ldx + 16 * it, wide) : zero;
+    uint32_t byte;
+    const uint2 c = item_codes<FMT>(y, g, &byte);
+    if (live)
+      for (int j = 0; j < p.topk; ++j)
+        if (row_of[j] >= 0) store_item<FMT>(p, row_of[j], srow_of[j], it, items, c, byte);
+  }
+}
+
 // ------------------------------------------------------------------ host side
 
 // Blocks of the item kernels: enough that each thread has about one item, but
@@ -387,6 +453,18 @@ Fp4QuantParams quant_params(const void* x, int64_t M, int64_t K, int64_t ldx, in
 }
 
 }  // namespace
+
+fp8q_status moe_plan_quant_small(const void* x, int64_t T, int64_t H, int64_t ldx, const int* ids, int topk, int E,
+                                 int format, const float* gscale, int* offsets, int* sf_offsets, int* pos, int* sf_row,
+                                 void* q, uint8_t* sf, cudaStream_t stream) {
+  Fp4QuantParams p = quant_params(x, T, H, ldx, format, gscale, q, H / 2, sf);
+  p.topk = topk;
+  const int wide = aligned(x, 32) && ldx % 16 == 0;
+  return launch_kernel(format == FP8Q_FP4_NV ? moe_small_kernel<kNv> : moe_small_kernel<kMx>,
+                       dim3(static_cast<unsigned>(T)), dim3(kItemThreads), 0, stream, 1, p, ids, E, offsets, sf_offsets,
+                       pos, sf_row, wide);
+}
+
 }  // namespace fp8q
 
 using namespace fp8q;

@@ -684,9 +684,15 @@ extern "C" fp8q_status fp8q_moe_experts_fp4(const void* x, int64_t T, int64_t ld
       !aligned(w13_gscale, 4) || !aligned(h_gscale, 4) || !aligned(w2_gscale, 4))
     return FP8Q_ERR_INVALID_ARG;
   if (E * 2 * I >= (int64_t{1} << 31) || E * H >= (int64_t{1} << 31)) return FP8Q_ERR_INVALID_ARG;
-  fp8q_status st = fp8q_moe_plan(ids, R, E, offsets, sf_offsets, pos, sf_row, b + sp.hist, sp.xq - sp.hist, stream);
-  if (st != FP8Q_OK) return st;
-  st = fp8q_moe_fp4_quant(x, T, H, ldx, topk, pos, sf_row, format, x_gscale, b + sp.xq, H / 2, b + sp.xsf, stream);
+  fp8q_status st;
+  if (R <= kSmallPlan) {
+    st = moe_plan_quant_small(x, T, H, ldx, ids, topk, static_cast<int>(E), format, x_gscale, offsets, sf_offsets, pos,
+                              sf_row, b + sp.xq, b + sp.xsf, static_cast<cudaStream_t>(stream));
+  } else {
+    st = fp8q_moe_plan(ids, R, E, offsets, sf_offsets, pos, sf_row, b + sp.hist, sp.xq - sp.hist, stream);
+    if (st != FP8Q_OK) return st;
+    st = fp8q_moe_fp4_quant(x, T, H, ldx, topk, pos, sf_row, format, x_gscale, b + sp.xq, H / 2, b + sp.xsf, stream);
+  }
   if (st != FP8Q_OK) return st;
   st = fp8q_grouped_mm_fp4_silu_quant(b + sp.xq, w13, b + sp.xsf, w13_sf, format, x_gscale, w13_gscale, offsets,
                                       sf_offsets, E, R, I, H, h_gscale, b + sp.hq, b + sp.hsf, stream);
