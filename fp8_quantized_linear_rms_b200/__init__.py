@@ -22,6 +22,7 @@ The names match the C ABI:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import NamedTuple
@@ -549,15 +550,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _launch_stream(stream, first: torch.Tensor, *rest) -> int | None:
+def _launch_stream(stream, *tensors) -> int | None:
     """The raw stream to launch on; every tensor must be on the current device
     (the kernels, and the outputs allocated for them, go there)."""
-    dev = first.get_device()
-    for t in rest:
+    dev = torch.cuda.current_device()
+    for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors must be on one device")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+            raise ValueError(f"all tensors must be on the current device, cuda:{dev}; one is on {t.device}")
     return _raw_stream(dev) if stream is None else _stream(stream)
 
 
@@ -577,7 +576,8 @@ def _empty(shape, dtype, like: torch.Tensor, stream):
 def _gscale(t, n: int, name: str):
     if t is None:
         return None
-    _need(t, torch.float32, name)
+    if type(t) is not torch.Tensor or t.dtype is not _F32 or not t.is_cuda:
+        _need(t, _F32, name)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must hold {n} contiguous value(s)")
     return t.data_ptr()
@@ -587,17 +587,22 @@ def _sf_shape(rows: int, K: int, group: int):
     return (-(-rows // 128), -(-K // (4 * group)), 512)
 
 
-def _need_sf(sf, rows: int, K: int, group: int, name: str, lead: int | None = None) -> int:
-    _need(sf, torch.uint8, name)
-    shape = _sf_shape(rows, K, group)
-    want = shape if lead is None else (lead, *shape)
-    if sf.numel() != shape[0] * shape[1] * 512 * (1 if lead is None else lead) or not sf.is_contiguous():
-        raise ValueError(f"{name} must be contiguous scale blocks {want}, got {tuple(sf.shape)}")
+_U8, _F32, _I32, _BF16 = torch.uint8, torch.float32, torch.int32, torch.bfloat16
+
+
+def _need_sf(sf, rows: int, K: int, group: int, name: str, lead: int = 1) -> int:
+    if type(sf) is not torch.Tensor or sf.dtype is not _U8 or not sf.is_cuda:
+        _need(sf, _U8, name)
+    n = -(-rows // 128) * -(-K // (4 * group)) * 512 * lead
+    if sf.numel() != n or not sf.is_contiguous():
+        raise ValueError(f"{name} must be contiguous scale blocks, {lead} x {_sf_shape(rows, K, group)}, "
+                         f"got {tuple(sf.shape)}")
     return sf.data_ptr()
 
 
 def _need_codes(q, name: str, dims: int = 2) -> None:
-    _need(q, torch.uint8, name)
+    if type(q) is not torch.Tensor or q.dtype is not _U8 or not q.is_cuda:
+        _need(q, _U8, name)
     if q.dim() != dims or not q.is_contiguous():
         raise ValueError(f"{name} must be contiguous packed codes with {dims} dimensions")
 
@@ -763,8 +768,9 @@ def fp8q_moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", b
 
 
 def _need_entries(t, dtype, T, k, name):
-    _need(t, dtype, name)
-    if tuple(t.shape) != (T, k) or not t.is_contiguous():
+    if type(t) is not torch.Tensor or t.dtype is not dtype or not t.is_cuda:
+        _need(t, dtype, name)
+    if t.shape != (T, k) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous [{T}, {k}]")
 
 
@@ -891,6 +897,11 @@ def make_moe_workspace(T: int, top_k: int, num_experts: int, H: int, I: int, fmt
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=1024)
+def _experts_bytes(T, k, E, H, I, f) -> int:
+    return lib.fp8q_moe_experts_fp4_workspace_bytes(T, k, E, H, I, f)
+
+
 def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor,
                          w13_sf: torch.Tensor, w2: torch.Tensor, w2_sf: torch.Tensor, fmt: str, x_gscale=None,
                          w13_gscale=None, h_gscale=None, w2_gscale=None, y=None, workspace=None, stream=None):
@@ -905,7 +916,7 @@ def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
     f, group = _fp4(fmt)
     (T, H), (E, I2, Hh) = x.shape, w13.shape
     I = I2 // 2
-    if Hh * 2 != H or I2 % 2 or tuple(w2.shape) != (E, H, I // 2):
+    if Hh * 2 != H or I2 % 2 or w2.shape != (E, H, I // 2):
         raise ValueError(f"x {tuple(x.shape)}, w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit")
     k = ids.shape[-1]
     _need_entries(ids, torch.int32, T, k, "ids")
@@ -915,8 +926,7 @@ def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
     g13, g2 = _gscale(w13_gscale, E, "w13_gscale"), _gscale(w2_gscale, E, "w2_gscale")
     y, ldy = _y_out(y, T, H, x, stream)
     if workspace is None:
-        n = lib.fp8q_moe_experts_fp4_workspace_bytes(T, k, E, H, I, f)
-        workspace = _empty((n,), torch.uint8, x, stream)
+        workspace = _empty((_experts_bytes(T, k, E, H, I, f),), _U8, x, stream)
     else:
         _need(workspace, torch.uint8, "workspace")
         if not workspace.is_contiguous():
