@@ -19,7 +19,7 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 struct RouteParams {
   const void* logits;        // fp32 or bf16 [T, E], leading dimension ld
   int64_t T, ld;
-  int E, bf16, vec, sigmoid;  // vec: rows begin at 16-byte boundaries
+  int E, bf16, vec, vec_bias, sigmoid;  // vec: rows, the biases, begin at 16-byte boundaries
   const float* bias;         // [E] or null
   int groups, topg, topk, renorm;
   float scale;
@@ -31,16 +31,31 @@ struct RouteParams {
 __device__ __forceinline__ float route_logit(const RouteParams& p, int64_t t, int e) {
   const float v = p.bf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.logits) + t * p.ld + e)) << 16)
                          : __ldg(static_cast<const float*>(p.logits) + t * p.ld + e);
-  return v != v ? -INFINITY : v + 0.0f;
+  return fmaxf(v, -INFINITY) + 0.0f;
 }
 
-// Bound of what the fp32 scores' errors make of the difference of two keys.  A
-// sigmoid: expf 2 ulp (2^-22), an addition and a division, below 2^-21 each.  A
-// softmax: the same and the rounded argument (d e^-d 2^-24), and the common
-// factor 1 / z, whose sum of at most 16 terms a lane and 5 levels is good to
-// 2^-19.2 of a difference of at most 1: together below 2^-18.  Twice that for
-// the sum of a group's two.  (The keys' own rounding is counted with them.)
-constexpr float kRouteError = 0x1p-17f;
+// Bounds of what the errors of the keys' fp32 scores make of the difference of
+// two groups' sums (of two keys: half).  With u = 2^-23, exp_approx(-d) is good
+// to (2 + d) u (ex2.approx to 2 u, the product with log2 e to 0.8 u d) and
+// rcp.approx to u, relative.  A sigmoid, with e = exp(-x): s (1 - s) (2 + |x|) u
+// + s u / 2 + s u < 2.2 u; four of them are below 2^-19.  A softmax, its
+// argument, reciprocal and product rounded too: p (4 + 1.5 d) u < 4.5 u, and the
+// common factor 1 / z, whose sum of at most 16 terms a lane and 5 levels is good
+// to 2^-19.2 of a difference of at most 1: together below 2^-18 for two, 2^-17
+// for four.  (The keys' own rounding is counted with them.)
+constexpr float kSigmoidError = 0x1p-19f;
+constexpr float kSoftmaxError = 0x1p-17f;
+
+__device__ __forceinline__ float exp_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // A lane's V logits of token t: experts [V lane, V lane + V), -inf beyond E.
 template <int V, bool BF16>
@@ -65,7 +80,7 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float x = __uint_as_float(BF16 ? (v & 1 ? w[v / 2] & 0xFFFF0000u : w[v / 2] << 16) : w[v]);
-        l[v] = x != x ? -INFINITY : x + 0.0f;
+        l[v] = fmaxf(x, -INFINITY) + 0.0f;
       }
       return;
     }
@@ -74,10 +89,27 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int
   for (int v = 0; v < V; ++v) l[v] = V * lane + v < p.E ? route_logit(p, t, V * lane + v) : -INFINITY;
 }
 
+// The biases of the lane's experts.
+template <int V>
+__device__ __forceinline__ void load_bias(const RouteParams& p, int lane, float* b) {
+  if constexpr (V >= 4) {
+    if (p.vec_bias && V * lane + V <= p.E) {
+#pragma unroll
+      for (int v = 0; v < V; v += 4) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(p.bias + V * lane + v));
+        b[v] = q.x, b[v + 1] = q.y, b[v + 2] = q.z, b[v + 3] = q.w;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) b[v] = V * lane + v < p.E ? __ldg(p.bias + V * lane + v) : 0.0f;
+}
+
 // Order-preserving integers of floating numbers; 0 is below all of them.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v);
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ uint64_t order_key(double v) {
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v));
@@ -99,43 +131,75 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
   return (static_cast<uint64_t>(mh) << 32) | ml;
 }
 
+// The keys of a lane in falling order (odd-even merge sort).
+template <int V, typename Key>
+__device__ __forceinline__ void sort_keys(Key (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+      for (int j = d % p; j + d < V; j += 2 * d)
+#pragma unroll
+        for (int i = j; i < j + d && i + d < V; ++i)
+          if (i / (2 * p) == (i + d) / (2 * p)) {
+            const Key a = k[i], b = k[i + d];
+            k[i] = a > b ? a : b;
+            k[i + d] = a > b ? b : a;
+          }
+}
+
 // The k largest keys of a token, one warp: lane holds experts [V lane, V lane +
 // V).  Groups first: a group counts with its largest key, or (TOP2) the sum of
 // its two largest; experts outside the best topg get key 0.  Equal keys go to
 // the lowest expert: the first lane's, and its first.  Returns lane j's j-th
-// expert.  32-bit keys of sums (TOP2) carry an error: `sure` is cleared where a
-// decision is closer than that.
+// expert.
+//
+// 32-bit keys of sums (TOP2) carry an error: `sure` is cleared where the groups,
+// or the set of experts, are decided by less than that.  There the experts go on
+// until one is apart from the next: `count` of them, whose order is only sure
+// if `ordered`.
+//
+// A lane sorts its keys once; a round then takes the largest head and moves its
+// owner's keys up; which experts they were is looked up for all at the end.
+// (Searching the lane's keys every round, with the groups' maxima one group
+// after another, took 1740 instructions a token and 23 us at 8192 tokens of 256
+// experts in 8 groups.)
 template <int V, typename Key, bool TOP2>
-__device__ __forceinline__ int route_select(const RouteParams& p, Key (&key)[V], int lane, bool& sure) {
+__device__ __forceinline__ int route_select(const RouteParams& p, Key (&key)[V], int lane, bool& sure,
+                                            int& count, bool& ordered) {
   constexpr bool ROUGH = TOP2 && sizeof(Key) == 4;
-  // a >= b are apart: |a - b| above the error of both
-  auto apart = [&](Key a, Key b) {
+  // a >= b are apart: |a - b| above the error of both, whose own rounding goes with `mag`
+  auto apart = [&](Key a, Key b, float mag) {
     if constexpr (ROUGH) {
       if (b <= order_key(-INFINITY)) return true;            // masked or excluded: exact
       const float x = key_float(a), y = key_float(b);
-      return x - y > kRouteError + 0x1p-21f * (fabsf(x) + fabsf(y));
+      return x - y > (p.sigmoid ? kSigmoidError : kSoftmaxError) + 0x1p-21f * (fabsf(x) + fabsf(y) + mag);
     }
     return true;
   };
   if (p.topg < p.groups) {
-    const int size = p.E / p.groups;
-    const bool whole = size % V == 0;   // a lane's experts lie in one group
-    Key t1 = 0, t2 = 0;
+    const int size = p.E / p.groups, span = size / V;
+    // a group's experts fill whole lanes, a power of two of them
+    const bool whole = span * V == size && (span & (span - 1)) == 0;
+    const int own = whole ? lane / span : lane;              // this lane's group, below p.groups
+    Key t1 = 0, t2 = 0;                                      // the two largest keys of group `own`
     if (whole) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (key[v] > t1) { t2 = t1; t1 = key[v]; }
-        else if (key[v] > t2) t2 = key[v];
+        const Key k = key[v], low = k < t1 ? k : t1;
+        t1 = k > t1 ? k : t1;
+        t2 = low > t2 ? low : t2;
       }
-    }
-    const int own = V * lane / size;
-    Key mine = 0;                       // lane g: group g's score
-    for (int g = 0; g < p.groups; ++g) {
-      Key a = 0, b = 0;                 // the lane's two largest of the group
-      if (whole) {
-        a = own == g ? t1 : 0;
-        b = own == g ? t2 : 0;
-      } else {
+      for (int o = 1; o < span; o <<= 1) {
+        const Key u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
+        const Key low = u1 < t1 ? u1 : t1, high = u2 > t2 ? u2 : t2;
+        t1 = u1 > t1 ? u1 : t1;
+        t2 = low > high ? low : high;
+      }
+    } else {
+      for (int g = 0; g < p.groups; ++g) {
+        Key a = 0, b = 0;                                    // of this lane
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const int e = V * lane + v;
@@ -144,94 +208,128 @@ __device__ __forceinline__ int route_select(const RouteParams& p, Key (&key)[V],
             else if (key[v] > b) b = key[v];
           }
         }
+        const Key first = warp_max(a);
+        const int owner = __ffs(__ballot_sync(kAll, a == first)) - 1;
+        const Key second = warp_max(lane == owner ? b : a);
+        if (lane == g) { t1 = first; t2 = second; }
       }
-      Key s = warp_max(a);
-      if constexpr (TOP2) {
-        if (size > 1) {
-          const int owner = __ffs(__ballot_sync(kAll, a == s)) - 1;
-          const Key second = warp_max(lane == owner ? b : a);
-          if constexpr (sizeof(Key) == 4) s = order_key(key_float(s) + key_float(second) + 0.0f);
-          else s = order_key(key_double(s) + key_double(second) + 0.0);
+    }
+    Key mine = t1;
+    float mag = 0.0f;
+    if constexpr (TOP2) {
+      if (size > 1) {
+        if constexpr (ROUGH) {
+          const float x = key_float(t1), y = key_float(t2);
+          mine = order_key(x + y + 0.0f);
+          // a sum may be far smaller than the two, and the errors with them
+          if (own < p.groups && y > -INFINITY) mag = fabsf(x) + fabsf(y);
+        } else {
+          mine = order_key(key_double(t1) + key_double(t2) + 0.0);
         }
       }
-      if (lane == g) mine = s;
     }
-    uint32_t keep = 0;
-    Key last = 0;
-    for (int j = 0; j <= p.topg; ++j) {
-      const Key s = warp_max(mine);
-      if (j == p.topg) {                // the best group left out
-        sure = sure && apart(last, s);
-        break;
-      }
-      last = s;
-      const int g = __ffs(__ballot_sync(kAll, mine == s && lane < p.groups && !((keep >> lane) & 1u))) - 1;
-      keep |= 1u << g;
-      if (lane == g) mine = 0;
+    // how many groups come before this lane's
+    const int step = whole ? span : 1;
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const Key other = __shfl_sync(kAll, mine, g * step);
+      rank += g < own ? other >= mine : other > mine;
     }
+    if (own >= p.groups) rank = p.groups;
+    if constexpr (ROUGH) {
+      const Key last = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == p.topg - 1)) - 1);
+      const Key next = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == p.topg)) - 1);
+      mag = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(mag)));     // not negative: ordered as integers
+      sure = sure && apart(last, next, mag);
+    }
+    const uint32_t keep = __ballot_sync(kAll, rank < p.topg);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = V * lane + v;
-      if (e >= p.E || !((keep >> (whole ? own : e / size)) & 1u)) key[v] = 0;
+      const int from = whole ? lane : min(31, (V * lane + v) / size);
+      if (!((keep >> from) & 1u)) key[v] = 0;
     }
   }
 
-  int id = 0;
-  Key last = 0;
-  const int rounds = ROUGH ? p.topk + 1 : p.topk;
-  for (int j = 0; j < rounds; ++j) {
-    Key a = 0;
+  Key head[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) a = key[v] > a ? key[v] : a;
-    const Key best = warp_max(a);
-    if (ROUGH && j > 0) sure = sure && apart(last, best);
-    if (j == p.topk) break;
-    last = best;
-    int e = 0;
-#pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] == best) e = v;
-    const int owner = __ffs(__ballot_sync(kAll, a == best)) - 1;
-    if (lane == owner) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v == e) key[v] = 0;
+  for (int v = 0; v < V; ++v) head[v] = key[v];
+  sort_keys<V>(head);
+  int owner = 0;                        // lane j: of the j-th key, `chosen`
+  Key chosen = 0, before = 0;
+  count = 0;
+  for (;;) {
+    const Key best = warp_max(head[0]);
+    if (count >= p.topk) {
+      if (!ROUGH || apart(before, best, 0.0f)) break;
+      if (count == 32) {
+        sure = false;
+        break;
+      }
     }
-    e = __shfl_sync(kAll, V * lane + e, owner);
-    if (lane == j) id = e;
+    const int o = __ffs(__ballot_sync(kAll, head[0] == best)) - 1;
+    if (lane == count) {
+      owner = o;
+      chosen = best;
+    }
+    if (lane == o) {
+#pragma unroll
+      for (int v = 0; v + 1 < V; ++v) head[v] = head[v + 1];
+      head[V - 1] = 0;
+    }
+    before = best;
+    ++count;
+  }
+  // equal keys of a lane follow one another: the how many-th of them this is
+  const Key above = __shfl_up_sync(kAll, chosen, 1);
+  const int owner_above = __shfl_up_sync(kAll, owner, 1);
+  const uint32_t firsts = __ballot_sync(kAll, lane == 0 || above != chosen || owner_above != owner);
+  int nth = lane - (31 - __clz(firsts & (0xFFFFFFFFu >> (31 - lane)))), id = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (__shfl_sync(kAll, key[v], owner) == chosen && nth-- == 0) id = V * owner + v;
+  ordered = true;
+  if constexpr (ROUGH) {
+    const Key next = __shfl_down_sync(kAll, chosen, 1);
+    ordered = __all_sync(kAll, lane + 1 >= count || apart(chosen, next, 0.0f));
   }
   return id;
 }
 
+constexpr int kRouteWarps = 4;          // tokens of a CTA
+
 // One warp a token.  Without a bias both scores grow with the logit, so the
 // order of the logits is the exact one.  With a bias the selection is decided
 // by score + bias in fp32 where the keys are further apart than its error
-// (kRouteError, and their rounding), else again in fp64: there two biased
-// scores that differ in exact arithmetic differ too, but for accidents below
-// 2^-50.  (fp64 for every token took 42 us at 8192 tokens of 256 experts.)
+// (above, and their rounding), else again in fp64, for the experts in question
+// where that settles it: there two biased scores that differ in exact arithmetic
+// differ too, but for accidents below 2^-50.  (fp64 for every token took 42 us
+// at 8192 tokens of 256 experts.)
 template <int V, bool BIASED, bool BF16>
-__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p) {
   const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   griddep_wait();
   griddep_launch_dependents();
   if (t >= p.T) return;
 
   float l[V];
   load_logits<V, BF16>(p, t, lane, l);
-  uint32_t top = 0;
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (V * lane + v < p.E) top = max(top, order_key(l[v]));
   // softmax: the largest logit and the sum of exponentials (terms equal to the
   // maximum count 1, infinite ones too); no sum where every logit is masked
   float m = 0.0f, z = 1.0f;
   if (!p.sigmoid) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) top = max(top, order_key(l[v]));
     m = key_float(warp_max(top));
     z = 0.0f;
+    if (fabsf(m) < INFINITY) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (l[v] > -INFINITY) z += l[v] == m ? 1.0f : expf(l[v] - m);
+      for (int v = 0; v < V; ++v) z += expf(l[v] - m);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) z += l[v] > -INFINITY && l[v] == m ? 1.0f : 0.0f;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
   }
@@ -240,24 +338,36 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
     return x > -INFINITY ? (x == m ? 1.0f : expf(x - m)) / z : 0.0f;
   };
 
-  int id;
-  bool sure = true;
+  int id, count;
+  bool sure = true, ordered = true;
   {
     uint32_t key[V];
+    if constexpr (BIASED) {
+      float b[V];
+      load_bias<V>(p, lane, b);
+      if (p.sigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = V * lane + v;
-      key[v] = 0;
-      if (e < p.E) {
-        float c = l[v];
-        if constexpr (BIASED) c = c > -INFINITY ? score(c) + __ldg(p.bias + e) + 0.0f : -INFINITY;
-        key[v] = order_key(c);
+        for (int v = 0; v < V; ++v) b[v] += rcp_approx(1.0f + exp_approx(-l[v]));
+      } else {
+        const float r = 1.0f / z;
+#pragma unroll
+        for (int v = 0; v < V; ++v) b[v] += l[v] == m ? r : exp_approx(l[v] - m) * r;
       }
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = order_key(l[v] > -INFINITY ? b[v] + 0.0f : -INFINITY);
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = order_key(l[v]);
     }
-    id = route_select<V, uint32_t, BIASED>(p, key, lane, sure);
+    if (V * lane + V > p.E) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (V * lane + v >= p.E) key[v] = 0;
+    }
+    id = route_select<V, uint32_t, BIASED>(p, key, lane, sure, count, ordered);
   }
   if constexpr (BIASED) {
-    if (!sure) {
+    if (!sure || !ordered) {
       double zd = 1.0;
       if (!p.sigmoid) {
         zd = 0.0;
@@ -269,23 +379,36 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(kAll, zd, o);
       }
-      uint64_t key[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = V * lane + v;
-        key[v] = 0;
-        if (e < p.E) {
-          double c = -INFINITY;
-          if (l[v] > -INFINITY) {
-            const double x = l[v];
-            const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x))
-                                       : (l[v] == m ? 1.0 : exp(x - static_cast<double>(m))) / zd;
-            c = s + static_cast<double>(__ldg(p.bias + e)) + 0.0;
-          }
-          key[v] = order_key(c);
+      auto exact = [&](float v, int e) {
+        double c = -INFINITY;
+        if (v > -INFINITY) {
+          const double x = v;
+          const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : (v == m ? 1.0 : exp(x - static_cast<double>(m))) / zd;
+          c = s + static_cast<double>(__ldg(p.bias + e)) + 0.0;
         }
+        return order_key(c);
+      };
+      if (sure) {
+        // the right experts, in an order that is not sure
+        const uint64_t mine = lane < count ? exact(route_logit(p, t, id), id) : 0;
+        int rank = 0, from = 0;
+        for (int j = 0; j < count; ++j) {
+          const uint64_t other = __shfl_sync(kAll, mine, j);
+          const int e = __shfl_sync(kAll, id, j);
+          rank += other > mine || (other == mine && e < id);
+        }
+        for (int j = 0; j < count; ++j)
+          if (__shfl_sync(kAll, rank, j) == lane) from = j;
+        id = __shfl_sync(kAll, id, from);
+      } else {
+        uint64_t key[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int e = V * lane + v;
+          key[v] = e < p.E ? exact(l[v], e) : 0;
+        }
+        id = route_select<V, uint64_t, true>(p, key, lane, sure, count, ordered);
       }
-      id = route_select<V, uint64_t, true>(p, key, lane, sure);
     }
   }
 
@@ -528,7 +651,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* o, int64_t
 
 template <int V>
 fp8q_status launch_route_v(const RouteParams& p, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.T + 7) / 8)), block(p.T < 8 ? 32 * static_cast<unsigned>(p.T) : 256);
+  const dim3 grid(static_cast<unsigned>((p.T + kRouteWarps - 1) / kRouteWarps));
+  const dim3 block(32 * static_cast<unsigned>(p.T < kRouteWarps ? p.T : kRouteWarps));
   auto kern = p.bias ? (p.bf16 ? route_kernel<V, true, true> : route_kernel<V, true, false>)
                      : (p.bf16 ? route_kernel<V, false, true> : route_kernel<V, false, false>);
   return launch_kernel(kern, grid, block, 0, s, 1, p);
@@ -597,7 +721,7 @@ extern "C" fp8q_status fp8q_moe_route(const void* logits, int logits_bf16, int64
   if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(ids, 4))
     return FP8Q_ERR_INVALID_ARG;
   const int vec = aligned(logits, 16) && ldl * (logits_bf16 ? 2 : 4) % 16 == 0;
-  const RouteParams p{logits, T, ldl, static_cast<int>(E), logits_bf16, vec, scoring == FP8Q_ROUTE_SIGMOID, bias,
+  const RouteParams p{logits, T, ldl, static_cast<int>(E), logits_bf16, vec, aligned(bias, 16), scoring == FP8Q_ROUTE_SIGMOID, bias,
                       num_groups, topk_groups, topk, renormalize, scale, weights, ids};
   return launch_route(p, static_cast<cudaStream_t>(stream));
 }

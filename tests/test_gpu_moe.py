@@ -75,6 +75,27 @@ def test_route_near_ties_with_a_bias():
     check_route(l, 8, scoring="sigmoid", bias=torch.zeros(E, device="cuda"))
 
 
+def test_route_groups_of_cancelling_biases():
+    """A group's two keys of +-4096 sum to little, with the roundings of 4096."""
+    E, T = 32, 400
+    g = torch.Generator(device="cuda").manual_seed(9)
+    l = torch.randn(T, E, device="cuda", generator=g)
+    bias = torch.zeros(E, device="cuda")
+    bias[0::4], bias[1::4], bias[2::4], bias[3::4] = 4096.0, -4096.0, -5000.0, -5000.0
+    check_route(l, 4, scoring="sigmoid", bias=bias, num_groups=8, topk_groups=4)
+    check_route(l, 4, scoring="softmax", bias=bias, num_groups=8, topk_groups=4)
+
+
+@pytest.mark.parametrize("E,G", [(48, 8), (96, 4), (256, 16), (512, 32), (240, 5)])
+def test_route_ties_between_groups(E, G):
+    """Equal groups and experts: the lowest first, whatever lanes hold them."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    l = torch.randint(-2, 3, (200, E), device="cuda", generator=g).float()
+    for bias in (None, torch.zeros(E, device="cuda")):
+        for scoring in ("softmax", "sigmoid"):
+            check_route(l, 6, scoring=scoring, bias=bias, num_groups=G, topk_groups=max(2, G // 3))
+
+
 def test_route_empty_and_refused():
     w, ids = fq.fp8q_moe_route(torch.zeros(0, 16, device="cuda"), 4)
     assert w.shape == ids.shape == (0, 4)
