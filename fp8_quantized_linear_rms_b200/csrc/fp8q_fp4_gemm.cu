@@ -327,8 +327,11 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
     }
   } else {
     for (int e = threadIdx.x; e < p.E; e += C::THREADS) {
-      const int first = __ldg(p.offsets + e), end = __ldg(p.offsets + e + 1);
-      ex[e] = {0, first, end - first, __ldg(p.sf_offsets + e)};
+      // whatever the arrays hold, rows stay below M and scales inside their buffer
+      const int M = static_cast<int>(p.M), first = min(max(__ldg(p.offsets + e), 0), M);
+      const int rows = min(max(__ldg(p.offsets + e + 1), first), M) - first;
+      const int most = M / 128 + min(M, p.E) - (rows + 127) / 128;
+      ex[e] = {0, first, rows, min(max(__ldg(p.sf_offsets + e), 0), most)};
     }
     __syncthreads();
     if (warp == 0) {

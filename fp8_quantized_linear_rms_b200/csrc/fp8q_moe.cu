@@ -435,6 +435,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanBlock = 4096;
+constexpr int64_t kMaxEntries = int64_t{1} << 25;   // every block reads all blocks' counts: a cost that grows with n^2
 
 struct PlanParams {
   const int* ids;
@@ -698,7 +699,7 @@ ExpertsSpace experts_space(int64_t T, int64_t topk, int64_t E, int64_t H, int64_
 bool experts_sizes(int64_t T, int topk, int64_t E, int64_t H, int64_t I, int format) {
   return (format == FP8Q_FP4_NV || format == FP8Q_FP4_MX) && T >= 0 && topk > 0 && topk <= kMaxTopk && E > 0 &&
          E <= kMaxExperts && H > 0 && H % 32 == 0 && I > 0 && H <= (1 << 24) && I <= (1 << 24) &&
-         T * topk < (int64_t{1} << 30);
+         T * topk <= kMaxEntries;
 }
 
 }  // namespace
@@ -735,7 +736,7 @@ extern "C" size_t fp8q_moe_plan_workspace_bytes(int64_t n, int64_t E) {
 extern "C" fp8q_status fp8q_moe_plan(const int* ids, int64_t n, int64_t E, int* offsets, int* sf_offsets, int* pos,
                                      int* sf_row, void* workspace, size_t ws_bytes, void* stream) {
   if (n < 0 || E <= 0 || n >= (int64_t{1} << 30)) return FP8Q_ERR_INVALID_ARG;
-  if (E > kMaxExperts) return FP8Q_ERR_UNSUPPORTED;
+  if (E > kMaxExperts || n > kMaxEntries) return FP8Q_ERR_UNSUPPORTED;
   if (!offsets || !sf_offsets || !aligned(offsets, 4) || !aligned(sf_offsets, 4)) return FP8Q_ERR_INVALID_ARG;
   if (n > 0 && (!ids || !pos || !sf_row || !aligned(ids, 4) || !aligned(pos, 4) || !aligned(sf_row, 4)))
     return FP8Q_ERR_INVALID_ARG;

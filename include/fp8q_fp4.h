@@ -142,7 +142,8 @@ FP8Q_API fp8q_status fp8q_moe_route(const void* logits, int logits_bf16, int64_t
  *   sf_row      int32 [n]: the row whose place its scales take, or -1
  *   workspace   fp8q_moe_plan_workspace_bytes(n, E) bytes (NULL if 0), of any
  *               content; calls that share one must not overlap in time
- * E <= 512 (else FP8Q_ERR_UNSUPPORTED).  The order never depends on timing.
+ * E <= 512, n <= 2^25 (else FP8Q_ERR_UNSUPPORTED).  The order never depends on
+ * timing.
  */
 FP8Q_API size_t fp8q_moe_plan_workspace_bytes(int64_t n, int64_t E);
 FP8Q_API fp8q_status fp8q_moe_plan(const int* ids, int64_t n, int64_t E, int* offsets, int* sf_offsets,
@@ -210,7 +211,7 @@ FP8Q_API fp8q_status fp8q_moe_combine(const void* o, int64_t ldo, const int* pos
  *   workspace   fp8q_moe_experts_fp4_workspace_bytes(...) bytes, 256-byte
  *               aligned, of any content; calls that share one must not overlap
  *               in time
- *   E <= 512, topk <= 32, H a multiple of 32, I of 128
+ *   E <= 512, topk <= 32, T topk <= 2^25, H a multiple of 32, I of 128
  */
 FP8Q_API size_t fp8q_moe_experts_fp4_workspace_bytes(int64_t T, int topk, int64_t E, int64_t H, int64_t I,
                                                      int format);

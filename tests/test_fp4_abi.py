@@ -166,3 +166,12 @@ def test_binding_refuses_what_is_not_on_a_gpu():
                  lambda: fq.fp8q_moe_experts_fp4(x, plan.pos, x, u[None], u, u[None], u, "nvfp4")):
         with pytest.raises(TypeError):
             call()
+
+
+def test_plan_of_more_entries_than_are_ordered():
+    big = (1 << 25) + 1
+    n = fq.fp8q_moe_plan_workspace_bytes(big, 4)
+    assert L.fp8q_moe_plan(P, big, 4, P, P, P, P, P, n, None) == UNS
+    assert L.fp8q_moe_plan(P, 1 << 30, 4, P, P, P, P, P, n, None) == BAD
+    assert experts(T=big, k=1, n=1 << 50) == BAD
+    assert fq.fp8q_moe_experts_fp4_workspace_bytes(big, 1, 8, 256, 128, "nvfp4") == 0
