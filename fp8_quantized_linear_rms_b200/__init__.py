@@ -548,12 +548,13 @@ def _fp4(fmt: str):
 # the raw current stream of a device, without the Stream object of the public call (3 us)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch_stream(stream, *tensors) -> int | None:
     """The raw stream to launch on; every tensor must be on the current device
     (the kernels, and the outputs allocated for them, go there)."""
-    dev = torch.cuda.current_device()
+    dev = _device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"all tensors must be on the current device, cuda:{dev}; one is on {t.device}")
@@ -573,6 +574,20 @@ def _empty(shape, dtype, like: torch.Tensor, stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+_U8, _F32, _I32, _BF16 = torch.uint8, torch.float32, torch.int32, torch.bfloat16
+
+
+def _rows(t, dtype, name: str):
+    """Rows, columns and row stride of a 2-D CUDA tensor with unit column stride (checked)."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or not t.is_cuda:
+        _need(t, dtype, name)
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1:
+        _rowmajor(t, name)                             # raises
+    M, K = t.shape
+    return M, K, stride[0]
+
+
 def _gscale(t, n: int, name: str):
     if t is None:
         return None
@@ -585,9 +600,6 @@ def _gscale(t, n: int, name: str):
 
 def _sf_shape(rows: int, K: int, group: int):
     return (-(-rows // 128), -(-K // (4 * group)), 512)
-
-
-_U8, _F32, _I32, _BF16 = torch.uint8, torch.float32, torch.int32, torch.bfloat16
 
 
 def _need_sf(sf, rows: int, K: int, group: int, name: str, lead: int = 1) -> int:
@@ -634,10 +646,8 @@ def fp8q_fp4_quant(x: torch.Tensor, fmt: str, gscale=None, q=None, sf=None, stre
     two e2m1 codes a byte; sf uint8 scale blocks of fp4_sf_shape).  fmt "nvfp4": groups of 16,
     e4m3 scales, value = code * scale * gscale (fp32 [1] on the device, or None); "mxfp4": groups
     of 32, E8M0 scales.  Also quantizes weights (a row is an output channel)."""
-    _need(x, torch.bfloat16, "x")
-    ldx = _rowmajor(x, "x")
+    M, K, ldx = _rows(x, _BF16, "x")
     f, group = _fp4(fmt)
-    M, K = x.shape
     g = _gscale(gscale, 1, "gscale")
     q, ldq, sf, sp = _fp4_quant_out(M, K, group, x, q, sf, stream)
     st = lib.fp8q_fp4_quant(x.data_ptr(), M, K, ldx, f, g, q.data_ptr(), ldq, sp,
@@ -649,11 +659,10 @@ def fp8q_fp4_quant(x: torch.Tensor, fmt: str, gscale=None, q=None, sf=None, stre
 def fp8q_rmsnorm_fp4_quant(x: torch.Tensor, w: torch.Tensor, eps: float, fmt: str, gscale=None, q=None,
                            sf=None, stream=None):
     """RMSNorm + 4-bit quantization; outputs as in fp8q_fp4_quant."""
-    _need(x, torch.bfloat16, "x")
-    _need(w, torch.bfloat16, "w")
-    ldx = _rowmajor(x, "x")
+    M, H, ldx = _rows(x, _BF16, "x")
+    if type(w) is not torch.Tensor or w.dtype is not _BF16 or not w.is_cuda:
+        _need(w, _BF16, "w")
     f, group = _fp4(fmt)
-    M, H = x.shape
     if w.numel() != H or not w.is_contiguous():
         raise ValueError(f"w must hold {H} contiguous values")
     g = _gscale(gscale, 1, "gscale")
@@ -666,10 +675,8 @@ def fp8q_rmsnorm_fp4_quant(x: torch.Tensor, w: torch.Tensor, eps: float, fmt: st
 
 def fp8q_silu_mul_fp4_quant(x: torch.Tensor, fmt: str, gscale=None, q=None, sf=None, stream=None):
     """SiLU*mul + 4-bit quantization of x [M, 2I] = [gate | up]; outputs [M, I] as in fp8q_fp4_quant."""
-    _need(x, torch.bfloat16, "x")
-    ldx = _rowmajor(x, "x")
+    M, I2, ldx = _rows(x, _BF16, "x")
     f, group = _fp4(fmt)
-    M, I2 = x.shape
     if I2 % 2:
         raise ValueError("x must have an even number of columns")
     I = I2 // 2
@@ -683,10 +690,9 @@ def fp8q_silu_mul_fp4_quant(x: torch.Tensor, fmt: str, gscale=None, q=None, sf=N
 
 def fp8q_fp4_dequant(q: torch.Tensor, sf: torch.Tensor, fmt: str, gscale=None, y=None, stream=None):
     """bf16 values [M, K] of packed codes q [M, K/2] and their scale blocks."""
-    _need(q, torch.uint8, "q")
-    ldq = _rowmajor(q, "q")
+    M, K2, ldq = _rows(q, _U8, "q")
+    K = 2 * K2
     f, group = _fp4(fmt)
-    M, K = q.shape[0], 2 * q.shape[1]
     sp = _need_sf(sf, M, K, group, "sf")
     g = _gscale(gscale, 1, "gscale")
     y, ldy = _y_out(y, M, K, q, stream)
@@ -808,10 +814,8 @@ def moe_sf_rows(n: int, num_experts: int) -> int:
 def fp8q_moe_fp4_quant(x: torch.Tensor, plan: MoePlan, fmt: str, gscale=None, stream=None):
     """fp8q_fp4_quant of tokens [T, H], each written to the rows of its experts.  Returns
     (q [T * top_k, H/2], sf) as fp8q_grouped_mm_fp4 reads them."""
-    _need(x, torch.bfloat16, "x")
-    ldx = _rowmajor(x, "x")
+    T, K, ldx = _rows(x, _BF16, "x")
     f, group = _fp4(fmt)
-    T, K = x.shape
     _need_entries(plan.pos, torch.int32, T, plan.pos.shape[1], "plan.pos")
     _need_entries(plan.sf_row, torch.int32, T, plan.pos.shape[1], "plan.sf_row")
     n = plan.pos.numel()
@@ -909,12 +913,11 @@ def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
     e = ids[t, j].  w13 codes [E, 2I, H/2] = [gate | up], w2 codes [E, H, I/2], with scale blocks
     [E, *fp4_sf_shape(rows, cols, fmt)]; x_gscale, h_gscale fp32 [1], w13_gscale, w2_gscale fp32 [E].
     Four launches for up to 128 (token, slot) entries, six at most; ids outside [0, E) add nothing."""
-    _need(x, torch.bfloat16, "x")
-    ldx = _rowmajor(x, "x")
+    T, H, ldx = _rows(x, _BF16, "x")
     _need_codes(w13, "w13", 3)
     _need_codes(w2, "w2", 3)
     f, group = _fp4(fmt)
-    (T, H), (E, I2, Hh) = x.shape, w13.shape
+    E, I2, Hh = w13.shape
     I = I2 // 2
     if Hh * 2 != H or I2 % 2 or w2.shape != (E, H, I // 2):
         raise ValueError(f"x {tuple(x.shape)}, w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit")
