@@ -2,9 +2,9 @@
 
 Argument marshalling only: every entry point takes torch CUDA tensors, checks
 dtypes and shapes enough to pass the right pointers, and calls the C ABI of
-``include/fp8q.h`` and ``include/fp8q_fp4.h`` with the current CUDA stream.  All arithmetic runs in the
-library's kernels; there is no CPU or PyTorch fallback, and importing this
-package fails loudly if ``libfp8q.so`` is missing (build it with
+``include/fp8q.h`` and ``include/fp8q_fp4.h`` with the current CUDA stream.
+All arithmetic runs in the library's kernels; there is no CPU or PyTorch
+fallback, and importing this package fails loudly if ``libfp8q.so`` is missing (build it with
 ``python fp8_quantized_linear_rms_b200/build.py``).
 
 The names match the C ABI:

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kItemThreads, OP == OP_SILU ? 4 : 6) fp4_items
       // so does the value between them (both are monotone): the exact value,
       // an fp64 chain of some thousand cycles, is needed only where they do not
       // (one in ~50 of the open brackets, themselves 5e-4 of the values).  What
-      // bounds the kernel is its instructions, ~40 a value (8192 x 12288 nvfp4:
+      // bounds the kernel is its instructions, 36 a value (8192 x 12288 nvfp4:
       // 153 us, 46% of HBM).  Tried and slower: a wider and cheaper bracket,
       // whose ends are both coded for every value (169 us); three or five CTAs
       // an SM (167, 152 with spills).
