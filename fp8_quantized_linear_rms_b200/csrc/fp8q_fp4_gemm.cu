@@ -61,8 +61,13 @@ struct Fp4Args {
   int stages, ring;            // stages of the ring, and its bytes (a split tile's part lies there too)
   int a_bytes;                 // shared memory of a stage's token tile
   int split;                   // CTAs that share a tile's depth
+  int share;                   // which rows of an expert: kAll, kPairs or kRest
   int* status;
 };
+
+// Experts' rows shared out between two launches: whole pairs of 128-row tiles
+// (the last may lack some of its second), and a remainder of at most 128 rows.
+constexpr int kAll = 0, kPairs = 1, kRest = 2;
 
 // One lane of a converged warp.  The TMA and tcgen05 instructions take uniform
 // registers; in code under elect.sync the compiler knows that one lane runs and
@@ -238,7 +243,7 @@ struct Fp4Cfg {
   static constexpr bool STAGED = !FUSED && !SPLIT;          // y leaves through shared memory
   static constexpr int OUT_BYTES = STAGED ? EPI_WARPS * 4096 : 0;
   static_assert(ACC_COLS + SFBUF * SF_TMEM <= TMEM, "tensor memory");
-  static_assert(!PAIR || (BN == 256 && !SPLIT && !FUSED), "pairs: dense, 256 columns");
+  static_assert(!PAIR || (BN == 256 && !SPLIT && !FUSED), "pairs: 256 columns");
   static_assert(!SPLIT || BN == 128, "split tiles have 128 columns");
 };
 
@@ -317,7 +322,10 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
     }
     __syncwarp();
   }
-  griddep_wait();
+  // The rest's launch follows the pairs', which had waited for what both read
+  // before it let this one start: it waits for the pairs themselves at its end,
+  // and takes the SMs that they leave one by one.
+  if (p.share != kRest) griddep_wait();
 
   constexpr int kTM = PAIR ? 256 : 128;
   if (p.offsets == nullptr) {
@@ -331,7 +339,13 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
       const int M = static_cast<int>(p.M), first = min(max(__ldg(p.offsets + e), 0), M);
       const int rows = min(max(__ldg(p.offsets + e + 1), first), M) - first;
       const int most = M / 128 + min(M, p.E) - (rows + 127) / 128;
-      ex[e] = {0, first, rows, min(max(__ldg(p.sf_offsets + e), 0), most)};
+      Fp4Expert x = {0, first, rows, min(max(__ldg(p.sf_offsets + e), 0), most)};
+      if (p.share != kAll) {
+        const int rest = (rows & 255) <= 128 ? rows & 255 : 0;
+        if (p.share == kPairs) x.rows -= rest;
+        else x = {0, first + rows - rest, rest, x.sf + (rows - rest) / 128};
+      }
+      ex[e] = x;
     }
     __syncthreads();
     if (warp == 0) {
@@ -724,6 +738,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
     if constexpr (PAIR) tmem_dealloc_pair(tmem, C::TMEM);
     else tmem_dealloc(tmem, C::TMEM);
   }
+  if (p.share == kRest) griddep_wait();
 }
 
 // ------------------------------------------------------------------ host side
@@ -783,8 +798,9 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
   if (!fp4_tensor_map(t, p.M, p.K, p.box, &mt) || !fp4_tensor_map(w, p.E * p.N, p.K, 128, &mw))
     return FP8Q_ERR_CUDA;
   if (PAIR) {
-    if (!fp4_scale_map(p.sft, (p.M + 127) / 128 * p.kb, C::NKB, &mts) ||
-        !fp4_scale_map(p.sfw, p.wblocks * p.kb, C::NKB, &mws))
+    const int64_t tblocks = p.offsets ? p.M / 128 + (p.M < p.E ? p.M : p.E) : (p.M + 127) / 128;
+    if (!fp4_scale_map(p.sft, tblocks * p.kb, C::NKB, &mts) ||
+        !fp4_scale_map(p.sfw, p.E * p.wblocks * p.kb, C::NKB, &mws))
       return FP8Q_ERR_CUDA;
   } else {
     mts = mt;      // not read
@@ -863,8 +879,13 @@ fp8q_status launch_fp4(const void* t, const void* w, int64_t tiles_t, Fp4Args& p
 //     mxfp4 (32 tiles) 9.7 split, 18.5 not; 1 x 10240 x 5120 (80) 11.2 and 11.0
 //   CTA pairs from as many 256 x 256 tiles as pairs of SMs: 512 x 10240 x 5120
 //     nvfp4 (80) 22.2 in pairs, 25.0 with 128 rows, 25.5 with 256; 256 x 5120 x
-//     5120 (20) 13, 10.6 and 12.9.  Experts' rows are ragged: pairs lost or
-//     drew everywhere (256 rows an expert, gate_up 88 in pairs, 83 without)
+//     5120 (20) 13, 10.6 and 12.9.  Experts' rows are ragged: pairs take the
+//     whole tiles, and the remainders, in a launch of their own, the SMs that
+//     the pairs leave.  Down products from 768 rows an expert on: 16 experts,
+//     4096 outputs of depth 2048, 1024 rows 91 without, 82-87 in pairs, 2048
+//     rows 224-230 and 149-160; 64, 2048 of 1408 mxfp4, 1024 rows 162-168 and
+//     121-138; 128, 2048 of 768, 256 rows 55 and 60, 512 rows 88-96 and 96-99,
+//     768 rows 188 and 159.  gate_up lost (256 rows 76 and 83) or drew
 //   256 weight rows unless 128 spread over the SMs in less than twice as many
 //     rounds: 1 x 51200 x 5120 (400 tiles of 128: 3 rounds, 200 of 256: 2) 29.4
 //     with 256, 26.2 with 128; 1 x 24576 x 4096 (2 and 1) 14.2 and 16.9
@@ -881,6 +902,15 @@ fp8q_status run_fp4(const void* t, const void* w, Fp4Args& p, cudaStream_t strea
   if constexpr (FUSED) {
     return launch_fp4<FMT, 128, true, false, false>(t, w, tt, p, stream);
   } else {
+    if (p.offsets && per >= 768) {
+      Fp4Args rest = p;
+      p.share = kPairs;
+      const fp8q_status st = launch_fp4<FMT, 256, false, true, false>(t, w, p.M / 129, p, stream);
+      if (st != FP8Q_OK) return st;
+      rest.share = kRest;
+      rest.box = 32;
+      return launch_fp4<FMT, 256, false, false, false>(t, w, p.M < p.E ? p.M : p.E, rest, stream);
+    }
     const int64_t pairs = (p.M + 255) / 256 * ((nw + 255) / 256);
     if (!p.offsets && p.M > 128 && 2 * pairs >= sms)
       return launch_fp4<FMT, 256, false, true, false>(t, w, (p.M + 255) / 256, p, stream);

@@ -211,6 +211,35 @@ def test_grouped_mm(fmt, T, k, E, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_rows_of_pairs_and_remainders(fmt):
+    """Experts of 768 rows and more on average: rows at both sides of 128 and 256, none, and one;
+    three calls one after the other."""
+    rows = [0, 1, 128, 129, 255, 256, 257, 384, 385, 512, 3 * 256 + 100, 9000]
+    E, N, K = len(rows), 272, 544
+    ids = torch.cat([torch.full((r,), e, dtype=torch.int32) for e, r in enumerate(rows)] + [torch.full((7,), -1, dtype=torch.int32)])
+    ids = ids[torch.randperm(len(ids), generator=torch.Generator().manual_seed(3))].view(-1, 1).cuda()
+    T = len(ids)
+    assert T >= 768 * E
+    plan = fq.fp8q_moe_plan(ids, E)
+    torch.manual_seed(12)
+    x = torch.randn(T, K, device="cuda").to(torch.bfloat16)
+    q, sf = fq.fp8q_moe_fp4_quant(x, plan, fmt)
+    w, wsf, wv = weights(E, N, K, fmt, 13)
+    y = torch.full((T, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    for _ in range(3):
+        fq.fp8q_grouped_mm_fp4(q, w, sf, wsf, fmt, plan, y=y)
+    assert fq.fp8q_last_device_status() == fq.OK
+    tok, exp = rows_of(plan)
+    xv = fq.fp8q_fp4_dequant(*fq.fp8q_fp4_quant(x, fmt), fmt).double()
+    for e in range(E):
+        at = np.nonzero(exp == e)[0]
+        assert at.size == rows[e]
+        if at.size:
+            check_mm(y[at], xv[tok[at]], wv[e], K, 1.0)
+    assert bool((y[tok.size:] == 3).all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("T,k,E,I,K", [(1, 2, 4, 128, 64), (20, 2, 8, 256, 160), (600, 3, 5, 384, 96), (2500, 2, 4, 2304, 128)])
 def test_silu_quant_epilogue(fmt, T, k, E, I, K):
     """Codes and scales of the quantized hidden rows.  The kernel's y differs from the definition's
