@@ -57,6 +57,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
+// e^(a - b), a <= b: what the difference's rounding leaves is added to first order.
+__device__ __forceinline__ float exp_diff(float a, float b) {
+  const float d = a - b;
+  if (!(d > -INFINITY)) return a == b ? 1.0f : 0.0f;         // infinite, or of two infinities
+  const float t = d - a, lo = (a - (d - t)) - (b + t), e = expf(d);
+  return fmaf(e, lo, e);
+}
+
 // A lane's V logits of token t: experts [V lane, V lane + V), -inf beyond E.
 template <int V, bool BF16>
 __device__ __forceinline__ void load_logits(const RouteParams& p, int64_t t, int lane, float* l) {
@@ -333,11 +341,6 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
   }
-  auto score = [&](float x) {
-    if (p.sigmoid) return 1.0f / (1.0f + expf(-x));
-    return x > -INFINITY ? (x == m ? 1.0f : expf(x - m)) / z : 0.0f;
-  };
-
   int id, count;
   bool sure = true, ordered = true;
   {
@@ -412,7 +415,21 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
     }
   }
 
-  float s = lane < p.topk ? score(route_logit(p, t, id)) : 0.0f;
+  // Weights.  A score below fp64's range counts as 0.  Renormalized, scores are
+  // taken relative to the largest selected logit (the sigmoid's: if negative),
+  // so that none is lost to fp32's range, however small they all are.
+  const float x = lane < p.topk ? route_logit(p, t, id) : -INFINITY;
+  const bool live = x > -INFINITY && (p.sigmoid ? x > -709.0f : x == m || x - m > -745.0f);
+  float top = p.sigmoid ? 0.0f : m;
+  if (p.renorm) {
+    const uint32_t k = warp_max(live ? order_key(x) : 0u);
+    if (k) top = p.sigmoid ? fminf(key_float(k), 0.0f) : key_float(k);
+  }
+  float s = 0.0f;
+  if (live) {
+    if (!p.sigmoid) s = p.renorm ? exp_diff(x, top) : exp_diff(x, top) / z;
+    else s = x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : exp_diff(x, top) / (1.0f + expf(x));
+  }
   if (p.renorm) {
     float sum = s;
 #pragma unroll

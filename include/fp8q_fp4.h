@@ -114,10 +114,12 @@ FP8Q_API fp8q_status fp8q_scaled_mm_fp4(const void* a_q, const void* b_q, const 
  *            equal groups of neighbours; a group counts with its largest key,
  *            or, with a bias, the sum of its two largest; experts outside the
  *            best topk_groups groups are not selected
- *   ids      the topk largest keys, descending; equal keys (and equal groups)
- *            go to the lowest index
+ *   ids      the topk largest keys, descending, as fp64 tells them apart; equal
+ *            keys (and equal groups) go to the lowest index
  *   weights  the scores of the selected experts, divided by their sum if
  *            renormalize is set (0 where that sum is 0), times scale
+ * Scores are those of fp64 (smaller ones count as 0), each good to 2^-19 of
+ * itself; an fp32 weight below 2^-126 may be 0.
  * A logit of -inf (or NaN) masks its expert: score 0, selected only after all
  * unmasked ones; a token whose experts are all masked has weights 0.
  *   E <= 512, topk <= 32, num_groups <= 32 (else FP8Q_ERR_UNSUPPORTED);

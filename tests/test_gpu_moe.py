@@ -395,3 +395,19 @@ def test_experts_graph_streams_and_workspace():
         fq.fp8q_moe_experts_fp4(x, ids, w, w13, s13, w2, s2, fmt, workspace=ws[256:512])
     with pytest.raises(ValueError):
         fq.fp8q_moe_experts_fp4(x, ids, w, w13, s13, w2[:, :, :64].contiguous(), s2, fmt)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_weights_of_small_scores(scoring, dtype):
+    """A bias that decides alone selects experts whose scores are far below the largest, and below
+    fp32's range: renormalized, their weights are those of fp64.  (The differences of logits near 100
+    are rounded at 2^-18: an exponential of them alone would miss the bound.)"""
+    T, E = 300, 64
+    g = torch.Generator(device="cuda").manual_seed(21)
+    l = (40 * torch.randn(T, E, device="cuda", generator=g)).to(dtype)
+    l[:100] -= 300
+    bias = 5000 * torch.randn(E, device="cuda", generator=g)
+    for renorm in (True, False):
+        check_route(l, 6, scoring=scoring, bias=bias, renormalize=renorm)
+        check_route(l, 6, scoring=scoring, renormalize=renorm)
