@@ -655,6 +655,10 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
             sfw |= s.byte << (8 * (j / G));
 #pragma unroll
             for (int i = 0; i < G; i += 8) code[(j + i) / 8] = fp4_codes8<FMT>(y + i, s);
+            if (fp4_far<FMT>(amax, s)) {
+#pragma unroll
+              for (int i = 0; i < G; i += 8) code[(j + i) / 8] = fp4_codes8_far(y + i, s);
+            }
           }
           uint4* q = reinterpret_cast<uint4*>(p.hq + static_cast<int64_t>(t.t0 + r) * (p.I >> 1) + (n >> 1));
 #pragma unroll

@@ -99,20 +99,19 @@ __device__ __forceinline__ Fp4Scale fp4_scale(float amax, const Fp4G& g) {
 // IEEE quotient fl32(y / d) by Markstein's division step (q0 = RN(y rcp), the
 // residual y - q0 d exact under FMA, RN(q0 + r rcp) = RN(y / d) for
 // rcp = RN(1/d)); a quotient too small for that argument rounds to code 0
-// either way.  mxfp4: rcp is a power of two, the product is the quotient.
-// The copied sign keeps -0; the minimum, which drops a NaN, gives an infinite y
-// (whose residual is NaN) the saturated code.
+// either way.  The residual is taken as q0 d - y and subtracted, so that a zero
+// quotient, of y = -0 or d = 0 too, keeps the sign of y.  mxfp4: rcp is a power
+// of two, the product is the quotient.
+// `far`: some quotient may be infinite (or of an infinite y), where that
+// residual would be NaN: the minimum, which drops a NaN, gives the saturated
+// code, and the sign is copied.
 // (Pairs of fp32 operations, .f32x2, were no faster: they cost the moves that
 // pair the registers.)
 template <int FMT>
-__device__ __forceinline__ uint32_t fp4_codes8(const float* y, const Fp4Scale& s) {
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float v = y[i] * s.rcp;
-    if constexpr (FMT == kNv) v = fminf(fabsf(fmaf(fmaf(-v, s.d, y[i]), s.rcp, v)), 8.0f);
-    q[i] = copysignf(v, y[i]);
-  }
+__device__ __forceinline__ bool fp4_far(float amax, const Fp4Scale& s) {
+  return FMT == kNv && !(amax * s.rcp < 0x1p100f);
+}
+__device__ __forceinline__ uint32_t fp4_cvt8(const float (&q)[8]) {
   uint32_t c;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -123,6 +122,25 @@ __device__ __forceinline__ uint32_t fp4_codes8(const float* y, const Fp4Scale& s
       : "=r"(c)
       : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
   return c;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t fp4_codes8(const float* y, const Fp4Scale& s) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    q[i] = y[i] * s.rcp;
+    if constexpr (FMT == kNv) q[i] = fmaf(-fmaf(q[i], s.d, -y[i]), s.rcp, q[i]);
+  }
+  return fp4_cvt8(q);
+}
+__device__ __forceinline__ uint32_t fp4_codes8_far(const float* y, const Fp4Scale& s) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = y[i] * s.rcp;
+    q[i] = copysignf(fminf(fabsf(fmaf(fmaf(-v, s.d, y[i]), s.rcp, v)), 8.0f), y[i]);
+  }
+  return fp4_cvt8(q);
 }
 
 // One value's code, in the low four bits.

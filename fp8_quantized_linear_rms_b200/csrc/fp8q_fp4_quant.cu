@@ -119,6 +119,11 @@ __device__ __forceinline__ uint2 item_codes(const Item& y, const Fp4G& g, uint32
   c.x = fp4_codes8<FMT>(f, s);
   chunk_to_f32(y.b, f);
   c.y = fp4_codes8<FMT>(f, s);
+  if (fp4_far<FMT>(amax, s)) {
+    c.y = fp4_codes8_far(f, s);
+    chunk_to_f32(y.a, f);
+    c.x = fp4_codes8_far(f, s);
+  }
   *byte = s.byte;
   return c;
 }
