@@ -68,27 +68,25 @@ __device__ __forceinline__ void st_item(uint16_t* p, const uint32_t (&o)[8], boo
 
 // Both ends of the bracket of bf16(silu(g) u) (the bounds of silu_pair): lo and
 // hi, bf16, |lo| <= |y| <= |hi|.  Chunks that the bracket does not serve (tiny
-// values or gates, gates below -85: tested on the packed bf16 words) are exact
-// at once.
-__device__ __forceinline__ uint32_t min_abs2(uint32_t m, uint32_t w) {
-  w &= 0x7FFF7FFFu;
-  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&m), *reinterpret_cast<const __nv_bfloat162*>(&w));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
+// values or gates, gates below -85) are exact at once; that is tested on the
+// packed bf16 words, whose magnitudes are ordered as integers.
 __device__ __forceinline__ uint4 silu_chunk(const uint4& g, const uint4& u, uint4& hi) {
   const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
-  uint32_t lo[4], h[4], least = 0x7F807F80u;        // smallest magnitude of gates and lower ends
+  constexpr uint32_t kMag = 0x7FFF7FFFu, kNeg85 = 0xC2AAu, kSmall = (127 - 99) << 7;    // bits of -85 and 2^-99
+  uint32_t lo[4], h[4], least = kMag, most = 0;     // smallest magnitude of gates and lower ends; largest gate, unsigned
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint64_t p = silu_p2(bf2_to_f2(gw[k]), bf2_to_f2(uw[k]));
-    lo[k] = f2_to_bf2_rn(mul2(p, dup2(kSiluLo)));
-    h[k] = f2_to_bf2_rn(mul2(p, dup2(kSiluHi)));
-    least = min_abs2(min_abs2(least, gw[k]), lo[k]);
+    const uint64_t g2 = bf2_to_f2(gw[k]);
+    const uint64_t np = mul2(mul2(g2, neg_sigmoid2(g2)), bf2_to_f2(uw[k]));          // -silu(g) u
+    lo[k] = f2_to_bf2_rn(mul2(np, dup2(-kSiluLo)));
+    h[k] = f2_to_bf2_rn(mul2(np, dup2(-kSiluHi)));
+    least = __vimin3_u16x2(least, gw[k] & kMag, lo[k] & kMag);
   }
+  most = __vmaxu2(__vimax3_u16x2(gw[0], gw[1], gw[2]), gw[3]);
   uint4 y = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   hi = make_uint4(h[0], h[1], h[2], h[3]);
-  // 2^-99: a lower end of at least that comes from a p above 2^-100
-  if (fminf(bf16_bits_to_f32(least & 0xFFFFu), bf16_bits_to_f32(least >> 16)) < 0x1p-99f || chunk_min_gate(g) < -85.0f)
+  // a lower end of 2^-99 at least comes from a p above 2^-100
+  if (min(least & 0xFFFFu, least >> 16) < kSmall || max(most & 0xFFFFu, most >> 16) > kNeg85)
     hi = y = silu_chunk_fix(g, u, y);
   return y;
 }
@@ -189,10 +187,11 @@ __global__ void __launch_bounds__(kItemThreads, OP == OP_SILU ? 4 : 6) fp4_items
       // so does the value between them (both are monotone): the exact value,
       // an fp64 chain of some thousand cycles, is needed only where they do not
       // (one in ~50 of the open brackets, themselves 5e-4 of the values).  What
-      // bounds the kernel is its instructions, 36 a value (8192 x 12288 nvfp4:
-      // 153 us, 46% of HBM).  Tried and slower: a wider and cheaper bracket,
-      // whose ends are both coded for every value (169 us); three or five CTAs
-      // an SM (167, 152 with spills).
+      // bounds the kernel is its instructions, ~31 a value (8192 x 12288: nvfp4
+      // 124 us, mxfp4 111, 57% and 63% of HBM).  Tried and slower: a wider and
+      // cheaper bracket, whose ends are both coded for every value (by 10%); open
+      // values coded pair by pair, each behind a vote (6%); three or five CTAs an
+      // SM (167, 152 with spills, when four took 153).
       Item hi = zero;
       const uint16_t* x = p.x + row * p.ldx + 16 * it;
       if (live) {

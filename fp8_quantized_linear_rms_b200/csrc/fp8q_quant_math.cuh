@@ -299,7 +299,7 @@ __device__ __forceinline__ uint64_t exp_neg2(uint64_t g2) {
 // (<= 2^-22.2), one rounding of 1 + e, the Newton-refined reciprocal
 // (<= 2^-23.9) and two multiplications: relative error <= 2^-21.0 while
 // nothing is tiny and the gate is >= -85 (within the fast exp's range).
-__device__ __forceinline__ uint64_t silu_p2(uint64_t g2, uint64_t u2) {
+__device__ __forceinline__ uint64_t neg_sigmoid2(uint64_t g2) {
   const uint64_t dd = add2(dup2(1.0f), exp_neg2(g2));
   float d0, d1;
   up2(dd, d0, d1);
@@ -307,9 +307,11 @@ __device__ __forceinline__ uint64_t silu_p2(uint64_t g2, uint64_t u2) {
   // -r1 = -r0 (1 + h); the result is within 2^-23.9 of 1/d.
   const uint64_t nr0 = pk2(rcp_approx(-d0), rcp_approx(-d1));
   const uint64_t h = fma2(dd, nr0, dup2(1.0f));
-  const uint64_t nr1 = fma2(nr0, h, nr0);
+  return fma2(nr0, h, nr0);
+}
+__device__ __forceinline__ uint64_t silu_p2(uint64_t g2, uint64_t u2) {
   // (-g)(-r1) u: negate g by its sign bits
-  return mul2(mul2(g2 ^ 0x8000000080000000ull, nr1), u2);
+  return mul2(mul2(g2 ^ 0x8000000080000000ull, neg_sigmoid2(g2)), u2);
 }
 
 // bf16 rounding of the low bracket end of a pair; `d` collects its XOR with
