@@ -66,28 +66,61 @@ __device__ __forceinline__ void st_item(uint16_t* p, const uint32_t (&o)[8], boo
   }
 }
 
-// Both ends of the bracket of bf16(silu(g) u) (the bounds of silu_pair): lo and
-// hi, bf16, |lo| <= |y| <= |hi|.  Chunks that the bracket does not serve (tiny
-// values or gates, gates below -85) are exact at once; that is tested on the
-// packed bf16 words, whose magnitudes are ordered as integers.
-__device__ __forceinline__ uint4 silu_chunk(const uint4& g, const uint4& u, uint4& hi) {
+// Both ends of the bracket of bf16(silu(g) u) (the bounds of silu_pair) in the
+// lanes of a word: lo and hi, bf16, |lo| <= |y| <= |hi|.
+__device__ __forceinline__ void silu_bracket(uint32_t gw, uint32_t uw, uint32_t& lo, uint32_t& hi) {
+  const uint64_t g2 = bf2_to_f2(gw);
+  const uint64_t np = mul2(mul2(g2, neg_sigmoid2(g2)), bf2_to_f2(uw));          // -silu(g) u
+  lo = f2_to_bf2_rn(mul2(np, dup2(-kSiluLo)));
+  hi = f2_to_bf2_rn(mul2(np, dup2(-kSiluHi)));
+}
+
+// The exact values of a chunk.
+__device__ __noinline__ uint4 silu_chunk_exact(const uint4 g, const uint4 u) {
+  uint4 lo, hi;
+  silu_bracket(g.x, u.x, lo.x, hi.x);
+  silu_bracket(g.y, u.y, lo.y, hi.y);
+  silu_bracket(g.z, u.z, lo.z, hi.z);
+  silu_bracket(g.w, u.w, lo.w, hi.w);
+  return silu_chunk_fix(g, u, lo);
+}
+
+// The bracket of a chunk; tested on the packed bf16 words, whose magnitudes are
+// ordered as integers:
+// - gates below -60, where |silu| <= 60 e^-60 < 2^-80: a signed zero, whose
+//   code is the value's unless the whole group is nearly as small; `wide`
+//   gathers the bound 2^-80 |up|.  (Exact values for them, as heavy-tailed
+//   gates have them one in 4000, took a seventh of the kernel's time.)
+// - other values or gates so small that the bracket does not serve: exact at once.
+__device__ __forceinline__ uint4 silu_chunk(const uint4& g, const uint4& u, uint4& hi, float& wide) {
   const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
-  constexpr uint32_t kMag = 0x7FFF7FFFu, kNeg85 = 0xC2AAu, kSmall = (127 - 99) << 7;    // bits of -85 and 2^-99
-  uint32_t lo[4], h[4], least = kMag, most = 0;     // smallest magnitude of gates and lower ends; largest gate, unsigned
+  constexpr uint32_t kMag = 0x7FFF7FFFu, kNeg60 = 0xC270u, kSmall = (127 - 99) << 7;   // bf16 bits
+  uint32_t lo[4], h[4], least = kMag;      // smallest magnitude of gates and lower ends
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint64_t g2 = bf2_to_f2(gw[k]);
-    const uint64_t np = mul2(mul2(g2, neg_sigmoid2(g2)), bf2_to_f2(uw[k]));          // -silu(g) u
-    lo[k] = f2_to_bf2_rn(mul2(np, dup2(-kSiluLo)));
-    h[k] = f2_to_bf2_rn(mul2(np, dup2(-kSiluHi)));
+    silu_bracket(gw[k], uw[k], lo[k], h[k]);
     least = __vimin3_u16x2(least, gw[k] & kMag, lo[k] & kMag);
   }
-  most = __vmaxu2(__vimax3_u16x2(gw[0], gw[1], gw[2]), gw[3]);
+  const uint32_t most = __vmaxu2(__vimax3_u16x2(gw[0], gw[1], gw[2]), gw[3]);       // the lowest negative gate
+  // a lower end of 2^-99 at least comes from a p above 2^-100
+  bool small = min(least & 0xFFFFu, least >> 16) < kSmall;
+  if (small || max(most & 0xFFFFu, most >> 16) > kNeg60) {
+    uint32_t largest = 0;                  // up of such a gate
+    least = kMag;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t far = __vcmpgtu2(gw[k], kNeg60 * 0x10001u), zero = ~uw[k] & 0x80008000u & far;
+      lo[k] = (lo[k] & ~far) | zero;
+      h[k] = (h[k] & ~far) | zero;
+      largest = __vmaxu2(largest, uw[k] & kMag & far);
+      least = __vimin3_u16x2(least, (gw[k] & kMag) | far, (lo[k] & kMag) | far);
+    }
+    wide = fmaxf(wide, bf16_bits_to_f32(max(largest & 0xFFFFu, largest >> 16)) * 0x1p-80f);
+    small = min(least & 0xFFFFu, least >> 16) < kSmall;
+  }
   uint4 y = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   hi = make_uint4(h[0], h[1], h[2], h[3]);
-  // a lower end of 2^-99 at least comes from a p above 2^-100
-  if (min(least & 0xFFFFu, least >> 16) < kSmall || max(most & 0xFFFFu, most >> 16) > kNeg85)
-    hi = y = silu_chunk_fix(g, u, y);
+  if (small) hi = y = silu_chunk_exact(g, u);
   return y;
 }
 
@@ -107,10 +140,10 @@ __device__ __forceinline__ void chunk_to_f32(const uint4& c, float* f) {
 // Codes and scale of one item, y already bf16.  mxfp4: every lane of a pair
 // must call it (shuffle); a lane without an item passes zeros.
 template <int FMT>
-__device__ __forceinline__ uint2 item_codes(const Item& y, const Fp4G& g, uint32_t* byte) {
-  float amax = absmax2_to_f32(chunk_absmax2(y.b, chunk_absmax2(y.a, 0u)));
+__device__ __forceinline__ uint2 item_codes(const Item& y, const Fp4G& g, Fp4Scale& s, float& amax) {
+  amax = absmax2_to_f32(chunk_absmax2(y.b, chunk_absmax2(y.a, 0u)));
   if constexpr (FMT == kMx) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-  const Fp4Scale s = fp4_scale<FMT>(amax, g);
+  s = fp4_scale<FMT>(amax, g);
   float f[8];
   uint2 c;
   chunk_to_f32(y.a, f);
@@ -122,6 +155,13 @@ __device__ __forceinline__ uint2 item_codes(const Item& y, const Fp4G& g, uint32
     chunk_to_f32(y.a, f);
     c.x = fp4_codes8_far(f, s);
   }
+  return c;
+}
+template <int FMT>
+__device__ __forceinline__ uint2 item_codes(const Item& y, const Fp4G& g, uint32_t* byte) {
+  Fp4Scale s;
+  float amax;
+  const uint2 c = item_codes<FMT>(y, g, s, amax);
   *byte = s.byte;
   return c;
 }
@@ -187,28 +227,34 @@ __global__ void __launch_bounds__(kItemThreads, OP == OP_SILU ? 4 : 6) fp4_items
       // so does the value between them (both are monotone): the exact value,
       // an fp64 chain of some thousand cycles, is needed only where they do not
       // (one in ~50 of the open brackets, themselves 5e-4 of the values).  What
-      // bounds the kernel is its instructions, ~31 a value (8192 x 12288: nvfp4
-      // 124 us, mxfp4 111, 57% and 63% of HBM).  Tried and slower: a wider and
-      // cheaper bracket, whose ends are both coded for every value (by 10%); open
-      // values coded pair by pair, each behind a vote (6%); three or five CTAs an
-      // SM (167, 152 with spills, when four took 153).
+      // bounds the kernel is its instructions, ~31 a value (8192 x 12288 nvfp4:
+      // 126 us of normal values, 132 of heavy-tailed ones, 55% of HBM).  Tried
+      // and slower: a wider and cheaper bracket, whose ends are both coded for
+      // every value (by 10%); open values coded pair by pair, each behind a vote
+      // (6%); three or five CTAs an SM (167, 152 with spills, when four took 153).
       Item hi = zero;
+      float bound = 0.0f;               // bound of the values that y has as zeros
       const uint16_t* x = p.x + row * p.ldx + 16 * it;
       if (live) {
         const Item gate = ld_item(x, wide), up = ld_item(x + p.K, wide);
-        y.a = silu_chunk(gate.a, up.a, hi.a);
-        y.b = silu_chunk(gate.b, up.b, hi.b);
+        y.a = silu_chunk(gate.a, up.a, hi.a, bound);
+        y.b = silu_chunk(gate.b, up.b, hi.b, bound);
       }
-      c = item_codes<FMT>(y, g, &byte);
+      Fp4Scale s;
+      float amax;
+      c = item_codes<FMT>(y, g, s, amax);
+      byte = s.byte;
       const bool open = differ(y.a, hi.a) || differ(y.b, hi.b);
-      if (__any_sync(0xFFFFFFFFu, open)) {
+      // a value below d / 5 has code 0; one of at most amax leaves the scale
+      const bool low = bound > 0.0f && (bound > amax || (s.d > 0.0f && bound >= 0.2f * s.d));
+      if (__any_sync(0xFFFFFFFFu, open || low)) {
         uint32_t byte2;
         const uint2 c2 = item_codes<FMT>(hi, g, &byte2);
-        if (__any_sync(0xFFFFFFFFu, byte != byte2 || c.x != c2.x || c.y != c2.y)) {
-          if (open) {                   // its inputs again, rather than in registers all along
+        if (__any_sync(0xFFFFFFFFu, low || byte != byte2 || c.x != c2.x || c.y != c2.y)) {
+          if (open || low) {            // its inputs again, rather than in registers all along
             const Item gate = ld_item(x, wide), up = ld_item(x + p.K, wide);
-            y.a = silu_chunk_fix(gate.a, up.a, y.a);
-            y.b = silu_chunk_fix(gate.b, up.b, y.b);
+            y.a = silu_chunk_exact(gate.a, up.a);
+            y.b = silu_chunk_exact(gate.b, up.b);
           }
           c = item_codes<FMT>(y, g, &byte);
         }

@@ -113,6 +113,32 @@ def test_silu_mul(fmt, M, I, ld):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_silu_mul_of_very_negative_gates(fmt):
+    """Gates at both sides of -60 and -85 and far below, beside ordinary ones and filling whole
+    groups (whose scale, with a small tensor scale, they then decide), with ups of every size."""
+    rng = np.random.default_rng(17)
+    M, I = 96, 256
+    gate = rng.standard_normal((M, I)).astype(np.float32)
+    up = rng.standard_normal((M, I)).astype(np.float32)
+    odd = np.array([-59.75, -60, -60.25, -61, -84.5, -85, -85.5, -88, -89, -100, -1e4, -3e38], np.float32)
+    at = rng.random((M, I)) < 0.05
+    gate[at] = rng.choice(odd, at.sum())
+    gate[32:64] = rng.uniform(-75, -45, (32, I))                       # small groups
+    gate[64:80] = rng.choice(odd, (16, I))
+    up[40:72] *= np.float32(2.0) ** rng.integers(-60, 90, (32, I))
+    up[80:] *= np.float32(1e30)
+    up[3, ::7], up[4, ::7], up[5, ::5] = 0.0, -0.0, 1e-30
+    up[6, 3], up[7, 3], up[66, 9] = np.inf, -np.inf, np.inf
+    gate[6, 3] = gate[7, 3] = gate[66, 9] = -70
+    x = inp.to_bf16_bits(np.concatenate([gate, up], 1))
+    v = values(x)
+    y = fp4.bf16(fp4.silu_mul(v[:, :I], v[:, I:]))
+    for g in (None, 2.0 ** -60, 2.0 ** 40) if fmt == "nvfp4" else (None,):
+        q, sf = fq.fp8q_silu_mul_fp4_quant(to_dev_bf16(x), fmt, gscale=gpu_g(g))
+        check(q, sf, y, fmt, g)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,K", [(1, 32), (130, 608), (1000, 4096)])
 def test_dequant(fmt, M, K):
     rng = np.random.default_rng(41)
