@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kItemThreads, OP == OP_SILU ? 4 : 6) fp4_items
       // so does the value between them (both are monotone): the exact value,
       // an fp64 chain of some thousand cycles, is needed only where they do not
       // (one in ~50 of the open brackets, themselves 5e-4 of the values).  What
-      // bounds the kernel is its instructions, ~31 a value (8192 x 12288 nvfp4:
+      // bounds the kernel is its instructions, 34 a value (8192 x 12288 nvfp4:
       // 126 us of normal values, 132 of heavy-tailed ones, 55% of HBM).  Tried
       // and slower: a wider and cheaper bracket, whose ends are both coded for
       // every value (by 10%); open values coded pair by pair, each behind a vote
