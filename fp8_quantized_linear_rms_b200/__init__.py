@@ -754,6 +754,8 @@ def fp8q_moe_route(logits: torch.Tensor, top_k: int, scoring: str = "softmax", b
         raise TypeError("logits must be a CUDA tensor")
     if logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if top_k <= 0:
+        raise ValueError("top_k must be positive")
     if scoring not in _SCORING:
         raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {scoring!r}")
     ld = _rowmajor(logits, "logits")
@@ -797,6 +799,8 @@ def fp8q_moe_plan(ids: torch.Tensor, num_experts: int, stream=None) -> MoePlan:
     _need(ids, torch.int32, "ids")
     if ids.dim() != 2 or not ids.is_contiguous():
         raise ValueError("ids must be contiguous [T, top_k]")
+    if num_experts <= 0:
+        raise ValueError("num_experts must be positive")
     n = ids.numel()
     offsets, sf_offsets = (_empty((num_experts + 1,), torch.int32, ids, stream) for _ in range(2))
     pos, sf_row = (_empty(ids.shape, torch.int32, ids, stream) for _ in range(2))
@@ -924,7 +928,9 @@ def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
     I = I2 // 2
     if Hh * 2 != H or I2 % 2 or w2.shape != (E, H, I // 2):
         raise ValueError(f"x {tuple(x.shape)}, w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit")
-    k = ids.shape[-1]
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise TypeError("ids must be a 2-D CUDA tensor")
+    k = ids.shape[1]
     _need_entries(ids, torch.int32, T, k, "ids")
     _need_entries(weights, torch.float32, T, k, "weights")
     s13, s2 = _need_sf(w13_sf, I2, H, group, "w13_sf", E), _need_sf(w2_sf, H, I, group, "w2_sf", E)

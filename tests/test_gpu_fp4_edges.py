@@ -216,3 +216,24 @@ def test_plans_and_rows_that_do_not_match_are_refused():
                 lambda: fq.fp8q_moe_plan(ids, 0)):
         with pytest.raises((ValueError, fq.Fp8qError)):
             bad()
+
+
+def test_arguments_that_are_refused_by_their_kind():
+    l = torch.zeros(3, 8, device="cuda")
+    for k in (0, -1):
+        with pytest.raises(ValueError):
+            fq.fp8q_moe_route(l, k)
+    with pytest.raises(fq.Fp8qError):
+        fq.fp8q_moe_route(torch.zeros(3, 64, device="cuda"), 33)
+    with pytest.raises(ValueError):
+        fq.fp8q_moe_plan(torch.zeros(3, 2, dtype=torch.int32, device="cuda"), -4)
+    with pytest.raises(TypeError):
+        fq.fp8q_moe_plan(torch.zeros(3, 2, dtype=torch.int64, device="cuda"), 4)
+    w13, s13, w2, s2 = experts_weights(2, 64, 128, "nvfp4", 90)
+    x, ids, w = rnd(3, 64), torch.zeros(3, 1, dtype=torch.int32, device="cuda"), torch.ones(3, 1, device="cuda")
+    good = [x, ids, w, w13, s13, w2, s2, "nvfp4"]
+    assert fq.fp8q_moe_experts_fp4(*good).shape == (3, 64)
+    for at, bad in ((0, x.float()), (0, x.cpu()), (1, ids.long()), (1, ids.tolist()), (1, ids[0]), (2, w.half()), (2, w[:2]),
+                    (3, w13[0]), (3, w13.float()), (4, s13[:1]), (5, w2.transpose(1, 2)), (6, s2.int()), (7, "fp4")):
+        with pytest.raises((TypeError, ValueError)):
+            fq.fp8q_moe_experts_fp4(*good[:at], bad, *good[at + 1:])
