@@ -38,12 +38,12 @@ __device__ __forceinline__ float route_logit(const RouteParams& p, int64_t t, in
 // two groups' sums (of two keys: half).  With u = 2^-23, exp_approx(-d) is good
 // to (2 + d) u (ex2.approx to 2 u, the product with log2 e to 0.8 u d) and
 // rcp.approx to u, relative.  A sigmoid, with e = exp(-x): s (1 - s) (2 + |x|) u
-// + s u / 2 + s u < 2.2 u; four of them are below 2^-19.  A softmax, its
+// + s u / 2 + s u < 2.2 u; four of them are below 9 u.  A softmax, its
 // argument, reciprocal and product rounded too: p (4 + 1.5 d) u < 4.5 u, and the
 // common factor 1 / z, whose sum of at most 16 terms a lane and 5 levels is good
 // to 2^-19.2 of a difference of at most 1: together below 2^-18 for two, 2^-17
-// for four.  (The keys' own rounding is counted with them.)
-constexpr float kSigmoidError = 0x1p-19f;
+// for four.  (The roundings of the keys and sums are counted with them.)
+constexpr float kSigmoidError = 0x1.2p-20f;
 constexpr float kSoftmaxError = 0x1p-17f;
 
 __device__ __forceinline__ float exp_approx(float x) {
@@ -157,107 +157,126 @@ __device__ __forceinline__ void sort_keys(Key (&k)[V]) {
           }
 }
 
-// The k largest keys of a token, one warp: lane holds experts [V lane, V lane +
-// V).  Groups first: a group counts with its largest key, or (TOP2) the sum of
-// its two largest; experts outside the best topg get key 0.  Equal keys go to
-// the lowest expert: the first lane's, and its first.  Returns lane j's j-th
-// expert.
+// Keys a >= b are apart: |a - b| above the error of both.  32-bit keys of scores
+// with a bias (ROUGH) have an error; that of a sum of two grows with their
+// magnitudes, `mag`.
+template <bool ROUGH, typename Key>
+__device__ __forceinline__ bool route_apart(const RouteParams& p, Key a, Key b, float mag) {
+  if constexpr (ROUGH) {
+    if (b <= order_key(-INFINITY)) return true;            // masked or excluded: exact
+    const float x = key_float(a), y = key_float(b);
+    return x - y > (p.sigmoid ? kSigmoidError : kSoftmaxError) + 0x1p-23f * (fabsf(x) + fabsf(y) + mag);
+  }
+  return true;
+}
+
+// Whether a group's experts fill whole lanes, a power of two of them.
+template <int V>
+__device__ __forceinline__ bool whole_groups(const RouteParams& p) {
+  const int size = p.E / p.groups, span = size / V;
+  return span * V == size && (span & (span - 1)) == 0;
+}
+
+// One warp a token: lane holds the keys of experts [V lane, V lane + V).  A group
+// counts with its largest key, or (TOP2) the sum of its two largest; equal groups
+// go to the lowest.  Returns the lanes' bits: of the lanes whose group is among
+// the best topg, or of lane g for group g where groups do not fill lanes
+// (route_keep reads it).  `sure` is cleared where 32-bit keys leave it open.
+template <int V, typename Key, bool TOP2>
+__device__ __forceinline__ uint32_t route_groups(const RouteParams& p, const Key (&key)[V], int lane, bool& sure) {
+  constexpr bool ROUGH = TOP2 && sizeof(Key) == 4;
+  const int size = p.E / p.groups, span = size / V;
+  const bool whole = whole_groups<V>(p);
+  const int own = whole ? lane / span : lane;              // this lane's group, below p.groups
+  Key t1 = 0, t2 = 0;                                      // the two largest keys of group `own`
+  if (whole) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const Key k = key[v], low = k < t1 ? k : t1;
+      t1 = k > t1 ? k : t1;
+      t2 = low > t2 ? low : t2;
+    }
+    for (int o = 1; o < span; o <<= 1) {
+      const Key u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
+      const Key low = u1 < t1 ? u1 : t1, high = u2 > t2 ? u2 : t2;
+      t1 = u1 > t1 ? u1 : t1;
+      t2 = low > high ? low : high;
+    }
+  } else {
+    for (int g = 0; g < p.groups; ++g) {
+      Key a = 0, b = 0;                                    // of this lane
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = V * lane + v;
+        if (e >= g * size && e < (g + 1) * size) {
+          if (key[v] > a) { b = a; a = key[v]; }
+          else if (key[v] > b) b = key[v];
+        }
+      }
+      const Key first = warp_max(a);
+      const int owner = __ffs(__ballot_sync(kAll, a == first)) - 1;
+      const Key second = warp_max(lane == owner ? b : a);
+      if (lane == g) { t1 = first; t2 = second; }
+    }
+  }
+  Key mine = t1;
+  float mag = 0.0f;
+  if constexpr (TOP2) {
+    if (size > 1) {
+      if constexpr (ROUGH) {
+        const float x = key_float(t1), y = key_float(t2);
+        mine = order_key(x + y + 0.0f);
+        // a sum may be far smaller than the two, and the errors with them
+        if (own < p.groups && y > -INFINITY) mag = fabsf(x) + fabsf(y);
+      } else {
+        mine = order_key(key_double(t1) + key_double(t2) + 0.0);
+      }
+    }
+  }
+  // how many groups come before this lane's
+  const int step = whole ? span : 1;
+  int rank = 0;
+  for (int g = 0; g < p.groups; ++g) {
+    const Key other = __shfl_sync(kAll, mine, g * step);
+    rank += g < own ? other >= mine : other > mine;
+  }
+  if (own >= p.groups) rank = p.groups;
+  if constexpr (ROUGH) {
+    const Key last = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == p.topg - 1)) - 1);
+    const Key next = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == p.topg)) - 1);
+    mag = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(mag)));     // not negative: ordered as integers
+    sure = sure && route_apart<ROUGH>(p, last, next, mag);
+  }
+  return __ballot_sync(kAll, rank < p.topg);
+}
+
+// Experts outside the groups of route_groups' bits get key 0.
+template <int V, typename Key>
+__device__ __forceinline__ void route_keep(const RouteParams& p, Key (&key)[V], int lane, uint32_t bits) {
+  const int size = p.E / p.groups;
+  const bool whole = whole_groups<V>(p);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int from = whole ? lane : min(31, (V * lane + v) / size);
+    if (!((bits >> from) & 1u)) key[v] = 0;
+  }
+}
+
+// The k largest keys; equal ones go to the lowest expert: the first lane's, and
+// its first.  Returns lane j's j-th expert.
 //
-// 32-bit keys of sums (TOP2) carry an error: `sure` is cleared where the groups,
-// or the set of experts, are decided by less than that.  There the experts go on
-// until one is apart from the next: `count` of them, whose order is only sure
-// if `ordered`.
+// ROUGH keys: the experts go on until one is apart from the next: `count` of
+// them, whose order is only sure if `ordered`; `sure` is cleared where 32 do not
+// settle the set.
 //
 // A lane sorts its keys once; a round then takes the largest head and moves its
 // owner's keys up; which experts they were is looked up for all at the end.
 // (Searching the lane's keys every round, with the groups' maxima one group
 // after another, took 1740 instructions a token and 23 us at 8192 tokens of 256
-// experts in 8 groups.)
-template <int V, typename Key, bool TOP2>
-__device__ __forceinline__ int route_select(const RouteParams& p, Key (&key)[V], int lane, bool& sure,
-                                            int& count, bool& ordered) {
-  constexpr bool ROUGH = TOP2 && sizeof(Key) == 4;
-  // a >= b are apart: |a - b| above the error of both, whose own rounding goes with `mag`
-  auto apart = [&](Key a, Key b, float mag) {
-    if constexpr (ROUGH) {
-      if (b <= order_key(-INFINITY)) return true;            // masked or excluded: exact
-      const float x = key_float(a), y = key_float(b);
-      return x - y > (p.sigmoid ? kSigmoidError : kSoftmaxError) + 0x1p-21f * (fabsf(x) + fabsf(y) + mag);
-    }
-    return true;
-  };
-  if (p.topg < p.groups) {
-    const int size = p.E / p.groups, span = size / V;
-    // a group's experts fill whole lanes, a power of two of them
-    const bool whole = span * V == size && (span & (span - 1)) == 0;
-    const int own = whole ? lane / span : lane;              // this lane's group, below p.groups
-    Key t1 = 0, t2 = 0;                                      // the two largest keys of group `own`
-    if (whole) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Key k = key[v], low = k < t1 ? k : t1;
-        t1 = k > t1 ? k : t1;
-        t2 = low > t2 ? low : t2;
-      }
-      for (int o = 1; o < span; o <<= 1) {
-        const Key u1 = __shfl_xor_sync(kAll, t1, o), u2 = __shfl_xor_sync(kAll, t2, o);
-        const Key low = u1 < t1 ? u1 : t1, high = u2 > t2 ? u2 : t2;
-        t1 = u1 > t1 ? u1 : t1;
-        t2 = low > high ? low : high;
-      }
-    } else {
-      for (int g = 0; g < p.groups; ++g) {
-        Key a = 0, b = 0;                                    // of this lane
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int e = V * lane + v;
-          if (e >= g * size && e < (g + 1) * size) {
-            if (key[v] > a) { b = a; a = key[v]; }
-            else if (key[v] > b) b = key[v];
-          }
-        }
-        const Key first = warp_max(a);
-        const int owner = __ffs(__ballot_sync(kAll, a == first)) - 1;
-        const Key second = warp_max(lane == owner ? b : a);
-        if (lane == g) { t1 = first; t2 = second; }
-      }
-    }
-    Key mine = t1;
-    float mag = 0.0f;
-    if constexpr (TOP2) {
-      if (size > 1) {
-        if constexpr (ROUGH) {
-          const float x = key_float(t1), y = key_float(t2);
-          mine = order_key(x + y + 0.0f);
-          // a sum may be far smaller than the two, and the errors with them
-          if (own < p.groups && y > -INFINITY) mag = fabsf(x) + fabsf(y);
-        } else {
-          mine = order_key(key_double(t1) + key_double(t2) + 0.0);
-        }
-      }
-    }
-    // how many groups come before this lane's
-    const int step = whole ? span : 1;
-    int rank = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      const Key other = __shfl_sync(kAll, mine, g * step);
-      rank += g < own ? other >= mine : other > mine;
-    }
-    if (own >= p.groups) rank = p.groups;
-    if constexpr (ROUGH) {
-      const Key last = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == p.topg - 1)) - 1);
-      const Key next = __shfl_sync(kAll, mine, __ffs(__ballot_sync(kAll, rank == p.topg)) - 1);
-      mag = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(mag)));     // not negative: ordered as integers
-      sure = sure && apart(last, next, mag);
-    }
-    const uint32_t keep = __ballot_sync(kAll, rank < p.topg);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int from = whole ? lane : min(31, (V * lane + v) / size);
-      if (!((keep >> from) & 1u)) key[v] = 0;
-    }
-  }
-
+// experts in 8 groups; now 1040 and 11.)
+template <int V, typename Key, bool ROUGH>
+__device__ __forceinline__ int route_select(const RouteParams& p, const Key (&key)[V], int lane, bool& sure, int& count,
+                                            bool& ordered) {
   Key head[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) head[v] = key[v];
@@ -268,7 +287,7 @@ __device__ __forceinline__ int route_select(const RouteParams& p, Key (&key)[V],
   for (;;) {
     const Key best = warp_max(head[0]);
     if (count >= p.topk) {
-      if (!ROUGH || apart(before, best, 0.0f)) break;
+      if (!ROUGH || route_apart<ROUGH>(p, before, best, 0.0f)) break;
       if (count == 32) {
         sure = false;
         break;
@@ -298,7 +317,7 @@ __device__ __forceinline__ int route_select(const RouteParams& p, Key (&key)[V],
   ordered = true;
   if constexpr (ROUGH) {
     const Key next = __shfl_down_sync(kAll, chosen, 1);
-    ordered = __all_sync(kAll, lane + 1 >= count || apart(chosen, next, 0.0f));
+    ordered = __all_sync(kAll, lane + 1 >= count || route_apart<ROUGH>(p, chosen, next, 0.0f));
   }
   return id;
 }
@@ -313,7 +332,7 @@ constexpr int kRouteWarps = 4;          // tokens of a CTA
 // differ too, but for accidents below 2^-50.  (fp64 for every token took 42 us
 // at 8192 tokens of 256 experts.)
 template <int V, bool BIASED, bool BF16>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps, V <= 8 ? 8 : 4) route_kernel(const RouteParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
   griddep_wait();
@@ -341,59 +360,83 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kAll, z, o);
   }
-  int id, count;
-  bool sure = true, ordered = true;
-  {
-    uint32_t key[V];
-    if constexpr (BIASED) {
-      float b[V];
-      load_bias<V>(p, lane, b);
-      if (p.sigmoid) {
+  uint32_t key[V];
+  if constexpr (BIASED) {
+    float b[V];
+    load_bias<V>(p, lane, b);
+    if (p.sigmoid) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) b[v] += rcp_approx(1.0f + exp_approx(-l[v]));
-      } else {
-        const float r = 1.0f / z;
+      for (int v = 0; v < V; ++v) b[v] += rcp_approx(1.0f + exp_approx(-l[v]));
+    } else {
+      const float r = 1.0f / z;
 #pragma unroll
-        for (int v = 0; v < V; ++v) b[v] += l[v] == m ? r : exp_approx(l[v] - m) * r;
+      for (int v = 0; v < V; ++v) b[v] += l[v] == m ? r : exp_approx(l[v] - m) * r;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = order_key(l[v] > -INFINITY ? b[v] + 0.0f : -INFINITY);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = order_key(l[v]);
+  }
+  if (V * lane + V > p.E) {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (V * lane + v >= p.E) key[v] = 0;
+  }
+
+  // fp64: the softmax's sum, an expert's key, the lane's keys
+  auto exact_sum = [&]() {
+    double zd = 1.0;
+    if (!p.sigmoid) {
+      zd = 0.0;
+#pragma unroll 1
+      for (int v = 0; v < V; ++v) {
+        const float x = V * lane + v < p.E ? route_logit(p, t, V * lane + v) : -INFINITY;
+        if (x > -INFINITY) zd += x == m ? 1.0 : exp(static_cast<double>(x) - static_cast<double>(m));
       }
 #pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = order_key(l[v] > -INFINITY ? b[v] + 0.0f : -INFINITY);
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) key[v] = order_key(l[v]);
+      for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(kAll, zd, o);
     }
-    if (V * lane + V > p.E) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (V * lane + v >= p.E) key[v] = 0;
+    return zd;
+  };
+  auto exact = [&](float v, int e, double zd) {
+    double c = -INFINITY;
+    if (v > -INFINITY) {
+      const double x = v;
+      const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : (v == m ? 1.0 : exp(x - static_cast<double>(m))) / zd;
+      c = s + static_cast<double>(__ldg(p.bias + e)) + 0.0;
     }
-    id = route_select<V, uint32_t, BIASED>(p, key, lane, sure, count, ordered);
+    return order_key(c);
+  };
+  auto exact_keys = [&](uint64_t (&k)[V], double zd) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = V * lane + v;
+      k[v] = e < p.E ? exact(l[v], e, zd) : 0;
+    }
+  };
+
+  bool sure = true, ordered = true;
+  uint32_t bits = kAll;
+  if (p.topg < p.groups) {
+    bits = route_groups<V, uint32_t, BIASED>(p, key, lane, sure);
+    if constexpr (BIASED) {
+      if (!sure) {
+        uint64_t k[V];
+        exact_keys(k, exact_sum());
+        bits = route_groups<V, uint64_t, true>(p, k, lane, sure);
+        sure = true;
+      }
+    }
+    route_keep<V>(p, key, lane, bits);
   }
+  int count, id = route_select<V, uint32_t, BIASED>(p, key, lane, sure, count, ordered);
   if constexpr (BIASED) {
     if (!sure || !ordered) {
-      double zd = 1.0;
-      if (!p.sigmoid) {
-        zd = 0.0;
-#pragma unroll 1
-        for (int v = 0; v < V; ++v) {
-          const float x = V * lane + v < p.E ? route_logit(p, t, V * lane + v) : -INFINITY;
-          if (x > -INFINITY) zd += x == m ? 1.0 : exp(static_cast<double>(x) - static_cast<double>(m));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) zd += __shfl_xor_sync(kAll, zd, o);
-      }
-      auto exact = [&](float v, int e) {
-        double c = -INFINITY;
-        if (v > -INFINITY) {
-          const double x = v;
-          const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : (v == m ? 1.0 : exp(x - static_cast<double>(m))) / zd;
-          c = s + static_cast<double>(__ldg(p.bias + e)) + 0.0;
-        }
-        return order_key(c);
-      };
+      const double zd = exact_sum();
       if (sure) {
         // the right experts, in an order that is not sure
-        const uint64_t mine = lane < count ? exact(route_logit(p, t, id), id) : 0;
+        const uint64_t mine = lane < count ? exact(route_logit(p, t, id), id, zd) : 0;
         int rank = 0, from = 0;
         for (int j = 0; j < count; ++j) {
           const uint64_t other = __shfl_sync(kAll, mine, j);
@@ -404,13 +447,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const RoutePara
           if (__shfl_sync(kAll, rank, j) == lane) from = j;
         id = __shfl_sync(kAll, id, from);
       } else {
-        uint64_t key[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int e = V * lane + v;
-          key[v] = e < p.E ? exact(l[v], e) : 0;
-        }
-        id = route_select<V, uint64_t, true>(p, key, lane, sure, count, ordered);
+        uint64_t k[V];
+        exact_keys(k, zd);
+        if (p.topg < p.groups) route_keep<V>(p, k, lane, bits);
+        id = route_select<V, uint64_t, false>(p, k, lane, sure, count, ordered);
       }
     }
   }
