@@ -248,7 +248,8 @@ struct Fp4Cfg {
 };
 
 template <int FMT, int CH, bool FUSED, bool PAIR, bool SPLIT>
-__global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::PER_SM)
+__global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS,
+                                  Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::PER_SM)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmT, const __grid_constant__ CUtensorMap tmW,
                     const __grid_constant__ CUtensorMap tmTS, const __grid_constant__ CUtensorMap tmWS,
                     const Fp4Args p) {
@@ -724,7 +725,8 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS, 
           if ((lane & 7) == 0)
             *reinterpret_cast<uint32_t*>(p.hq + static_cast<int64_t>(t.t0 + row) * (p.I >> 1) + (n >> 1)) = code;
           if (lane % G == 0)
-            p.hsf[fp4_sf_offset(static_cast<int64_t>(t.tblk) * 128 + row, n / G, fp4_kblocks(FMT, p.I))] = static_cast<uint8_t>(sc.byte);
+            p.hsf[fp4_sf_offset(static_cast<int64_t>(t.tblk) * 128 + row, n / G, fp4_kblocks(FMT, p.I))] =
+                static_cast<uint8_t>(sc.byte);
         } else if (row < t.cnt && n < p.N) {
           *reinterpret_cast<uint4*>(p.y + static_cast<int64_t>(t.t0 + row) * p.ldy + n) =
               make_uint4(pack_bf16(v[0] * alpha, v[1] * alpha), pack_bf16(v[2] * alpha, v[3] * alpha),
@@ -963,7 +965,8 @@ fp8q_status check_y(void* y, int64_t ldy, int64_t M, int64_t N, Fp4Args* p) {
 }
 
 fp8q_status check_groups(const int* offsets, const int* sf_offsets, int64_t M, Fp4Args* p) {
-  if (M > 0 && (!offsets || !sf_offsets || !aligned(offsets, 4) || !aligned(sf_offsets, 4))) return FP8Q_ERR_INVALID_ARG;
+  if (M > 0 && (!offsets || !sf_offsets || !aligned(offsets, 4) || !aligned(sf_offsets, 4)))
+    return FP8Q_ERR_INVALID_ARG;
   p->offsets = offsets;
   p->sf_offsets = sf_offsets;
   return FP8Q_OK;

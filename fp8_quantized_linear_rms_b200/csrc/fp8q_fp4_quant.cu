@@ -194,7 +194,8 @@ __device__ __forceinline__ void emit_item(const Fp4QuantParams& p, int64_t row, 
 
 // Row of item i of `total`; a 32-bit division where it serves.
 __device__ __forceinline__ int64_t item_row(int64_t i, int items, int64_t total) {
-  return total <= 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(items)) : i / items;
+  return total <= 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(i) / static_cast<uint32_t>(items))
+                             : i / items;
 }
 
 // Plain and SiLU*mul: independent items, one a thread and step.  A warp takes 32
@@ -204,7 +205,8 @@ __device__ __forceinline__ int64_t item_row(int64_t i, int items, int64_t total)
 constexpr int kItemThreads = 256;
 
 template <int FMT, int OP>
-__global__ void __launch_bounds__(kItemThreads, OP == OP_SILU ? 4 : 6) fp4_items_kernel(const Fp4QuantParams p, int wide) {
+__global__ void __launch_bounds__(kItemThreads, OP == OP_SILU ? 4 : 6)
+    fp4_items_kernel(const Fp4QuantParams p, int wide) {
   const int items = static_cast<int>(p.K >> 4);
   const int64_t total = p.M * items;
   griddep_wait();
@@ -412,7 +414,8 @@ __global__ void __launch_bounds__(kItemThreads)
   };
   auto blocks_below = [&](int e) {
     int c = 0;
-    for (int w = 0; w <= (e - 1) >> 5; ++w) c += __popc(w == e >> 5 ? present[w] & ((1u << (e & 31)) - 1u) : present[w]);
+    for (int w = 0; w <= (e - 1) >> 5; ++w)
+      c += __popc(w == e >> 5 ? present[w] & ((1u << (e & 31)) - 1u) : present[w]);
     return c;
   };
   const int64_t t = blockIdx.x;

@@ -29,8 +29,9 @@ struct RouteParams {
 
 // A NaN counts as -inf (masked); -0 as 0, so that keys are equal where values are.
 __device__ __forceinline__ float route_logit(const RouteParams& p, int64_t t, int e) {
-  const float v = p.bf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p.logits) + t * p.ld + e)) << 16)
-                         : __ldg(static_cast<const float*>(p.logits) + t * p.ld + e);
+  const int64_t i = t * p.ld + e;
+  const float v = p.bf16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(p.logits) + i))
+                         : __ldg(static_cast<const float*>(p.logits) + i);
   return fmaxf(v, -INFINITY) + 0.0f;
 }
 
@@ -674,7 +675,8 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* o, int64_t
   griddep_wait();
   griddep_launch_dependents();
   const int64_t cols = H >> 3, total = T * cols;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t t = i / cols;
     const int64_t c = (i - t * cols) * 8;
     float acc[8] = {};
@@ -738,7 +740,8 @@ ExpertsSpace experts_space(int64_t T, int64_t topk, int64_t E, int64_t H, int64_
     at += (bytes + 255) / 256 * 256;
     return r;
   };
-  const int64_t R = T * topk, blocks = R / 128 + (R < E ? R : E);   // scale block rows: every expert's last may be ragged
+  // scale block rows: every expert's last may be ragged
+  const int64_t R = T * topk, blocks = R / 128 + (R < E ? R : E);
   w.pos = take(R * 4);
   w.sf_row = take(R * 4);
   w.offsets = take((E + 1) * 4);
@@ -772,15 +775,16 @@ extern "C" fp8q_status fp8q_moe_route(const void* logits, int logits_bf16, int64
   if (scoring != FP8Q_ROUTE_SOFTMAX && scoring != FP8Q_ROUTE_SIGMOID) return FP8Q_ERR_INVALID_ARG;
   if (renormalize != 0 && renormalize != 1) return FP8Q_ERR_INVALID_ARG;
   if (E > kMaxExperts || topk > kMaxTopk || num_groups > 32) return FP8Q_ERR_UNSUPPORTED;
-  if (E % num_groups != 0 || topk_groups > num_groups || topk > E / num_groups * topk_groups) return FP8Q_ERR_INVALID_ARG;
+  if (E % num_groups != 0 || topk_groups > num_groups || topk > E / num_groups * topk_groups)
+    return FP8Q_ERR_INVALID_ARG;
   if (T >= (int64_t{1} << 31)) return FP8Q_ERR_INVALID_ARG;
   if (T == 0) return FP8Q_OK;
   if (!logits || !weights || !ids) return FP8Q_ERR_INVALID_ARG;
   if (!aligned(logits, logits_bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(weights, 4) || !aligned(ids, 4))
     return FP8Q_ERR_INVALID_ARG;
   const int vec = aligned(logits, 16) && ldl * (logits_bf16 ? 2 : 4) % 16 == 0;
-  const RouteParams p{logits, T, ldl, static_cast<int>(E), logits_bf16, vec, aligned(bias, 16), scoring == FP8Q_ROUTE_SIGMOID, bias,
-                      num_groups, topk_groups, topk, renormalize, scale, weights, ids};
+  const RouteParams p{logits, T, ldl, static_cast<int>(E), logits_bf16, vec, aligned(bias, 16),
+                      scoring == FP8Q_ROUTE_SIGMOID, bias, num_groups, topk_groups, topk, renormalize, scale, weights, ids};
   return launch_route(p, static_cast<cudaStream_t>(stream));
 }
 
@@ -811,7 +815,8 @@ extern "C" fp8q_status fp8q_moe_plan(const int* ids, int64_t n, int64_t E, int* 
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FP8Q_ERR_CUDA;
   if (!attr_done[dev].load(std::memory_order_relaxed)) {
     for (auto k : {plan_count_kernel, plan_place_kernel})
-      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanWarps * (kMaxExperts + 1) * 4) != cudaSuccess)
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanWarps * (kMaxExperts + 1) * 4) !=
+          cudaSuccess)
         return FP8Q_ERR_CUDA;
     attr_done[dev].store(1, std::memory_order_relaxed);
   }
