@@ -325,7 +325,8 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS,
   }
   // The rest's launch follows the pairs', which had waited for what both read
   // before it let this one start: it waits for the pairs themselves at its end,
-  // and takes the SMs that they leave one by one.
+  // and takes the SMs that they leave one by one.  (Plain loads go to L2, past
+  // what an L1 may hold of an earlier call's.)
   if (p.share != kRest) griddep_wait();
 
   constexpr int kTM = PAIR ? 256 : 128;
@@ -337,10 +338,10 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS,
   } else {
     for (int e = threadIdx.x; e < p.E; e += C::THREADS) {
       // whatever the arrays hold, rows stay below M and scales inside their buffer
-      const int M = static_cast<int>(p.M), first = min(max(__ldg(p.offsets + e), 0), M);
-      const int rows = min(max(__ldg(p.offsets + e + 1), first), M) - first;
+      const int M = static_cast<int>(p.M), first = min(max(__ldcg(p.offsets + e), 0), M);
+      const int rows = min(max(__ldcg(p.offsets + e + 1), first), M) - first;
       const int most = M / 128 + min(M, p.E) - (rows + 127) / 128;
-      Fp4Expert x = {0, first, rows, min(max(__ldg(p.sf_offsets + e), 0), most)};
+      Fp4Expert x = {0, first, rows, min(max(__ldcg(p.sf_offsets + e), 0), most)};
       if (p.share != kAll) {
         const int rest = (rows & 255) <= 128 ? rows & 255 : 0;
         if (p.share == kPairs) x.rows -= rest;
@@ -377,11 +378,11 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS,
   // SPLIT: the tile, and the factors that its output takes, before the long wait
   Fp4Tile tile0{};
   const Fp4G gh = fp4_g(FUSED ? p.gh : nullptr);
-  const float ga = p.ga ? *p.ga : 1.0f;
+  const float ga = p.ga ? __ldcg(p.ga) : 1.0f;
   float gb = 1.0f;
   if (SPLIT && cta < units) {
     tile0 = fp4_tile<PAIR>(p, ex, cta, CH, 0);
-    if (p.gb) gb = p.gb[tile0.e];
+    if (p.gb) gb = __ldcg(p.gb + tile0.e);
   }
   // a wait by the whole warp; false in all lanes if one gave up
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(Fp4Cfg<FMT, CH, FUSED, PAIR, SPLIT>::THREADS,
     bool ok = true;
     for (int u = cta; ok && u < units; u += ctas) {
       const Fp4Tile t = SPLIT ? tile0 : fp4_tile<PAIR>(p, ex, u, CH, rank);
-      if (!SPLIT && p.gb) gb = p.gb[t.e];      // on its way while the tile is computed
+      if (!SPLIT && p.gb) gb = __ldcg(p.gb + t.e);      // on its way while the tile is computed
       if constexpr (SPLIT) {
         // This CTA's part of the tile, fp32, over the ring (whose copies and MMAs
         // are done): row r at r BN, 16-byte chunks XORed by the row.

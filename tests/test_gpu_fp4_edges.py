@@ -237,3 +237,45 @@ def test_arguments_that_are_refused_by_their_kind():
                     (3, w13[0]), (3, w13.float()), (4, s13[:1]), (5, w2.transpose(1, 2)), (6, s2.int()), (7, "fp4")):
         with pytest.raises((TypeError, ValueError)):
             fq.fp8q_moe_experts_fp4(*good[:at], bad, *good[at + 1:])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_replayed_pairs_and_remainders_follow_their_inputs(fmt):
+    """Experts of many rows (whole tiles and remainders in two launches), captured once: every replay
+    on other ids, tokens and expert scales gives what a call gives."""
+    T, E, N, K = 4000, 4, 1024, 256
+    w = [fq.fp8q_fp4_quant(rnd(N, K, seed=300 + e), fmt) for e in range(E)]
+    b, bsf = torch.stack([v[0] for v in w]), torch.stack([v[1] for v in w])
+    x, ids = rnd(T, K, seed=310), torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    gb = torch.ones(E, device="cuda") if fmt == "nvfp4" else None
+
+    def run():
+        plan = fq.fp8q_moe_plan(ids, E)
+        q, sf = fq.fp8q_moe_fp4_quant(x, plan, fmt)
+        o = fq.fp8q_grouped_mm_fp4(q, b, sf, bsf, fmt, plan, b_gscale=gb)
+        return fq.fp8q_moe_combine(o, plan, torch.ones(T, 1, device="cuda"))
+
+    run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run()
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    for i in range(12):
+        x.copy_(rnd(T, K, seed=320 + i))
+        share = torch.rand(E, device="cuda", generator=gen) + 0.01
+        ids.copy_(torch.multinomial(share, T, replacement=True, generator=gen).int().view(T, 1))
+        if gb is not None:
+            gb.copy_(torch.rand(E, device="cuda", generator=gen) + 0.5)
+        for _ in range(2):
+            graph.replay()
+        got = y.clone()
+        assert torch.equal(got, run())
+        # row by row: a token's row depends on its expert alone
+        for e in range(E):
+            rows = torch.nonzero(ids[:, 0] == e)[:100, 0]
+            if len(rows):
+                q, sf = fq.fp8q_fp4_quant(x[rows], fmt)
+                d = fq.fp8q_scaled_mm_fp4(q, b[e], sf, bsf[e], fmt, b_gscale=None if gb is None else gb[e:e + 1]).double()
+                # the same products in another order: fp32 accumulation, then a rounding to bf16
+                assert bool(((got[rows].double() - d).abs() <= 2.0 ** -6 * d.abs() + 2.0 ** -12 * d.abs().mean()).all())
+    assert fq.fp8q_last_device_status() == fq.OK
