@@ -919,7 +919,8 @@ def fp8q_moe_experts_fp4(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tens
     """The experts' pass over tokens x bf16 [T, H]: y[t] = sum_j weights[t, j] W2_e quant(silu(gate) up),
     e = ids[t, j].  w13 codes [E, 2I, H/2] = [gate | up], w2 codes [E, H, I/2], with scale blocks
     [E, *fp4_sf_shape(rows, cols, fmt)]; x_gscale, h_gscale fp32 [1], w13_gscale, w2_gscale fp32 [E].
-    Four launches for up to 128 (token, slot) entries, six at most; ids outside [0, E) add nothing."""
+    Four launches for up to 128 (token, slot) entries, five to seven for more; ids outside [0, E) add
+    nothing."""
     T, H, ldx = _rows(x, _BF16, "x")
     _need_codes(w13, "w13", 3)
     _need_codes(w2, "w2", 3)

@@ -4,8 +4,11 @@ that do not fit, alignments, experts without rows."""
 import subprocess
 import sys
 
+import numpy as np
 import pytest
 import torch
+
+from oracle import fp4
 
 pytestmark = pytest.mark.gpu
 
@@ -279,3 +282,14 @@ def test_replayed_pairs_and_remainders_follow_their_inputs(fmt):
                 # the same products in another order: fp32 accumulation, then a rounding to bf16
                 assert bool(((got[rows].double() - d).abs() <= 2.0 ** -6 * d.abs() + 2.0 ** -12 * d.abs().mean()).all())
     assert fq.fp8q_last_device_status() == fq.OK
+
+
+@pytest.mark.parametrize("n,E", [(8192, 512), (28673, 3), (32768, 500), (32769, 64), (45000, 512), (300000, 128)])
+def test_plan_of_many_entries(n, E):
+    """Both sides of a plan whose blocks are one cluster, back to back on other ids."""
+    rng = np.random.default_rng(n)
+    for _ in range(3):
+        ids = rng.integers(-1, E + 1, (n, 1)).astype(np.int32)
+        p = fq.fp8q_moe_plan(torch.from_numpy(ids).cuda(), E)
+        for got, want, name in zip(p, fp4.plan(ids, E), p._fields):
+            np.testing.assert_array_equal(got.cpu().numpy(), want, err_msg=name)
