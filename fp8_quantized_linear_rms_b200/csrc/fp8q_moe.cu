@@ -509,8 +509,10 @@ struct PlanParams {
 };
 
 // A warp's part of a block: kPlanSteps steps of 32 entries, read at once (a
-// load a step would wait out the latency of each).  Absent or foreign experts
-// become -1.
+// load a step would wait out the latency of each).  Every id outside [0, E)
+// becomes -1, whose low bits are no expert's: same_lanes looks at those only,
+// so another negative id (ids less the first expert that is here) would count
+// as the expert whose low bits it has.
 constexpr int kPlanSteps = kPlanBlock / kPlanWarps / 32;
 
 __device__ __forceinline__ void plan_load(const PlanParams& p, int i0, int lane, int* e) {
@@ -521,7 +523,7 @@ __device__ __forceinline__ void plan_load(const PlanParams& p, int i0, int lane,
   }
 #pragma unroll
   for (int k = 0; k < kPlanSteps; ++k)
-    if (e[k] >= p.E) e[k] = -1;
+    if (static_cast<unsigned>(e[k]) >= static_cast<unsigned>(p.E)) e[k] = -1;
 }
 
 // Lanes of the warp with the same value of the low `bits` bits.
