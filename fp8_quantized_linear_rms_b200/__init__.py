@@ -874,6 +874,8 @@ def fp8q_grouped_mm_fp4_silu_quant(a_q: torch.Tensor, b_q: torch.Tensor, a_sf: t
     [E, 2I, K/2] = [gate | up] rows, I a multiple of 128.  Returns (q [M, I/2], sf) at the plan's
     rows, with tensor scale `gscale`."""
     f, group, M, N, K, E, ga, gb = _grouped(a_q, b_q, a_sf, b_sf, fmt, plan, a_gscale, b_gscale)
+    if N % 2:
+        raise ValueError(f"b_q must have as many up rows as gate rows, got {N} in all")
     g = _gscale(gscale, 1, "gscale")
     I = N // 2
     q = _empty((M, I // 2), torch.uint8, a_q, stream)
