@@ -91,32 +91,40 @@ __device__ __noinline__ uint4 silu_chunk_exact(const uint4 g, const uint4 u) {
 //   code is the value's unless the whole group is nearly as small; `wide`
 //   gathers the bound 2^-80 |up|.  (Exact values for them, as heavy-tailed
 //   gates have them one in 4000, took a seventh of the kernel's time.)
-// - other values or gates so small that the bracket does not serve: exact at once.
+// - other values or gates so small that the bracket does not serve, and gates
+//   above 2^127, whose exponential's argument may overflow: exact at once.
 __device__ __forceinline__ uint4 silu_chunk(const uint4& g, const uint4& u, uint4& hi, float& wide) {
   const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
-  constexpr uint32_t kMag = 0x7FFF7FFFu, kNeg60 = 0xC270u, kSmall = (127 - 99) << 7;   // bf16 bits
-  uint32_t lo[4], h[4], least = kMag;      // smallest magnitude of gates and lower ends
+  constexpr uint32_t kMag = 0x7FFF7FFFu, k60 = 0x4270u, kNeg60 = 0xC270u, kSmall = (127 - 99) << 7;   // bf16 bits
+  constexpr int kHuge = 0x7F00;            // 2^127
+  uint32_t lo[4], h[4], gm[4], least = kMag;      // smallest magnitude of gates and lower ends
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     silu_bracket(gw[k], uw[k], lo[k], h[k]);
-    least = __vimin3_u16x2(least, gw[k] & kMag, lo[k] & kMag);
+    gm[k] = gw[k] & kMag;
+    least = __vimin3_u16x2(least, gm[k], lo[k] & kMag);
   }
-  const uint32_t most = __vmaxu2(__vimax3_u16x2(gw[0], gw[1], gw[2]), gw[3]);       // the lowest negative gate
+  const uint32_t most = __vmaxu2(__vimax3_u16x2(gm[0], gm[1], gm[2]), gm[3]);       // the gate furthest from 0
   // a lower end of 2^-99 at least comes from a p above 2^-100
   bool small = min(least & 0xFFFFu, least >> 16) < kSmall;
-  if (small || max(most & 0xFFFFu, most >> 16) > kNeg60) {
-    uint32_t largest = 0;                  // up of such a gate
-    least = kMag;
+  if (small || max(most & 0xFFFFu, most >> 16) > k60) {
+    const uint32_t low = __vmaxu2(__vimax3_u16x2(gw[0], gw[1], gw[2]), gw[3]);      // the lowest negative gate
+    if (max(low & 0xFFFFu, low >> 16) > kNeg60) {
+      uint32_t largest = 0;                // up of such a gate
+      least = kMag;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t far = __vcmpgtu2(gw[k], kNeg60 * 0x10001u), zero = ~uw[k] & 0x80008000u & far;
-      lo[k] = (lo[k] & ~far) | zero;
-      h[k] = (h[k] & ~far) | zero;
-      largest = __vmaxu2(largest, uw[k] & kMag & far);
-      least = __vimin3_u16x2(least, (gw[k] & kMag) | far, (lo[k] & kMag) | far);
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t far = __vcmpgtu2(gw[k], kNeg60 * 0x10001u), zero = ~uw[k] & 0x80008000u & far;
+        lo[k] = (lo[k] & ~far) | zero;
+        h[k] = (h[k] & ~far) | zero;
+        largest = __vmaxu2(largest, uw[k] & kMag & far);
+        least = __vimin3_u16x2(least, gm[k] | far, (lo[k] & kMag) | far);
+      }
+      wide = fmaxf(wide, bf16_bits_to_f32(max(largest & 0xFFFFu, largest >> 16)) * 0x1p-80f);
+      small = min(least & 0xFFFFu, least >> 16) < kSmall;
     }
-    wide = fmaxf(wide, bf16_bits_to_f32(max(largest & 0xFFFFu, largest >> 16)) * 0x1p-80f);
-    small = min(least & 0xFFFFu, least >> 16) < kSmall;
+    const uint32_t top = __vmaxs2(__vimax3_s16x2(gw[0], gw[1], gw[2]), gw[3]);      // the largest gate
+    small |= max(static_cast<int16_t>(top & 0xFFFFu), static_cast<int16_t>(top >> 16)) > kHuge;
   }
   uint4 y = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   hi = make_uint4(h[0], h[1], h[2], h[3]);
@@ -230,7 +238,7 @@ __global__ void __launch_bounds__(kItemThreads, OP == OP_SILU ? 4 : 6)
       // an fp64 chain of some thousand cycles, is needed only where they do not
       // (one in ~50 of the open brackets, themselves 5e-4 of the values).  What
       // bounds the kernel is its instructions, 34 a value (8192 x 12288 nvfp4:
-      // 126 us of normal values, 132 of heavy-tailed ones, 55% of HBM).  Tried
+      // 128 us of normal values, 135 of heavy-tailed ones, 53% of HBM).  Tried
       // and slower: a wider and cheaper bracket, whose ends are both coded for
       // every value (by 10%); open values coded pair by pair, each behind a vote
       // (6%); three or five CTAs an SM (167, 152 with spills, when four took 153).

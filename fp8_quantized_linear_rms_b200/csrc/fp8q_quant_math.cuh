@@ -314,10 +314,18 @@ __device__ __forceinline__ uint64_t silu_p2(uint64_t g2, uint64_t u2) {
   return mul2(mul2(g2 ^ 0x8000000080000000ull, neg_sigmoid2(g2)), u2);
 }
 
+// The smaller of two values, a NaN if one of them is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // bf16 rounding of the low bracket end of a pair; `d` collects its XOR with
 // the high end; `bad` is set for tiny values, tiny gates (g (1/(1+e^-g)) would
 // be an fp32 subnormal short of bits, which a large up value can lift back into
-// range) and gates below -85.
+// range), gates below -85 and gates whose product with log2 e overflows (above
+// 2.35e38: exp_neg2 and p are then NaN, though the value may be ordinary).
 __device__ __forceinline__ uint32_t silu_pair(uint32_t gw, uint32_t uw, uint32_t& d, bool& bad) {
   const uint64_t g2 = bf2_to_f2(gw);
   const uint64_t p = silu_p2(g2, bf2_to_f2(uw));
@@ -326,7 +334,7 @@ __device__ __forceinline__ uint32_t silu_pair(uint32_t gw, uint32_t uw, uint32_t
   float p0, p1, g0, g1;
   up2(p, p0, p1);
   up2(g2, g0, g1);
-  bad |= fminf(fminf(fabsf(p0), fabsf(p1)), fminf(fabsf(g0), fabsf(g1))) < kTiny || fminf(g0, g1) < -85.0f;
+  bad |= !(min_nan(min_nan(fabsf(p0), fabsf(p1)), fminf(fabsf(g0), fabsf(g1))) >= kTiny) || fminf(g0, g1) < -85.0f;
   return na;
 }
 
@@ -358,7 +366,7 @@ __device__ __noinline__ uint4 silu_chunk_fix(const uint4 g, const uint4 u, uint4
     up2(u2, uf[0], uf[1]);
     bool need = open != 0;
     for (int h = 0; h < 2; ++h)
-      need |= gf[h] < -85.0f ||
+      need |= gf[h] < -85.0f || gf[h] > 0x1p127f ||
               ((fabsf(pf[h]) < kTiny || fabsf(gf[h]) < kTiny) && gf[h] != 0.0f && uf[h] != 0.0f);
     if (need) yw[k] = silu_pair_f64(gw[k], uw[k]);
   }
