@@ -899,7 +899,10 @@ extern "C" fp8q_status fp8q_moe_experts_fp4(const void* x, int64_t T, int64_t ld
       !aligned(w13_sf, 16) || !aligned(w2, 16) || !aligned(w2_sf, 16) || !aligned(x_gscale, 4) ||
       !aligned(w13_gscale, 4) || !aligned(h_gscale, 4) || !aligned(w2_gscale, 4))
     return FP8Q_ERR_INVALID_ARG;
-  if (E * 2 * I >= (int64_t{1} << 31) || E * H >= (int64_t{1} << 31)) return FP8Q_ERR_INVALID_ARG;
+  constexpr int64_t kMax32 = int64_t{1} << 31;          // rows of all weights, tiles
+  const int64_t tiles = R / 128 + E;
+  if (E * 2 * I >= kMax32 || E * H >= kMax32 || tiles * ((2 * I + 63) / 64) >= kMax32 || tiles * ((H + 63) / 64) >= kMax32)
+    return FP8Q_ERR_INVALID_ARG;
   fp8q_status st;
   if (R <= kSmallPlan) {
     st = moe_plan_quant_small(x, T, H, ldx, ids, topk, static_cast<int>(E), format, x_gscale, offsets, sf_offsets, pos,
