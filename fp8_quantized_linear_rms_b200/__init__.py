@@ -581,14 +581,15 @@ _U8, _F32, _I32, _BF16 = torch.uint8, torch.float32, torch.int32, torch.bfloat16
 
 
 def _rows(t, dtype, name: str):
-    """Rows, columns and row stride of a 2-D CUDA tensor with unit column stride (checked)."""
+    """Rows, columns and row stride of a 2-D CUDA tensor with unit column stride (checked).  A single
+    row counts as contiguous, whatever stride it carries."""
     if type(t) is not torch.Tensor or t.dtype is not dtype or not t.is_cuda:
         _need(t, dtype, name)
     stride = t.stride()
     if len(stride) != 2 or stride[1] != 1:
         _rowmajor(t, name)                             # raises
     M, K = t.shape
-    return M, K, stride[0]
+    return M, K, stride[0] if M > 1 else K
 
 
 def _gscale(t, n: int, name: str):
@@ -637,7 +638,7 @@ def _fp4_quant_out(M, K, group, x, q, sf, stream):
         _need(q, torch.uint8, "q")
         if tuple(q.shape) != (M, K // 2):
             raise ValueError(f"q must be [{M}, {K // 2}]")
-        ldq = _rowmajor(q, "q")
+        ldq = _rows(q, _U8, "q")[2]
     if sf is None:
         sf = _empty(_sf_shape(M, K, group), torch.uint8, x, stream)
         return q, ldq, sf, sf.data_ptr()
@@ -712,7 +713,7 @@ def _y_out(y, M, N, like, stream):
     _need(y, torch.bfloat16, "y")
     if tuple(y.shape) != (M, N):
         raise ValueError(f"y must be [{M}, {N}]")
-    return y, _rowmajor(y, "y")
+    return y, _rows(y, _BF16, "y")[2]
 
 
 def fp8q_scaled_mm_fp4(a_q: torch.Tensor, b_q: torch.Tensor, a_sf: torch.Tensor, b_sf: torch.Tensor, fmt: str,
@@ -890,15 +891,14 @@ def fp8q_grouped_mm_fp4_silu_quant(a_q: torch.Tensor, b_q: torch.Tensor, a_sf: t
 
 def fp8q_moe_combine(o: torch.Tensor, plan: MoePlan, weights: torch.Tensor, y=None, stream=None):
     """y [T, H] bf16 = the sum over slots of weights [T, top_k] times rows plan.pos of o (bf16)."""
-    _need(o, torch.bfloat16, "o")
+    n, H, ldo = _rows(o, _BF16, "o")
     T, k = plan.pos.shape
     _need_entries(plan.pos, torch.int32, T, k, "plan.pos")
     _need_entries(weights, torch.float32, T, k, "weights")
-    if o.shape[0] != T * k:
+    if n != T * k:
         raise ValueError(f"o must have {T * k} rows")
-    H = o.shape[1]
     y, ldy = _y_out(y, T, H, o, stream)
-    st = lib.fp8q_moe_combine(o.data_ptr(), _rowmajor(o, "o"), plan.pos.data_ptr(), weights.data_ptr(), T, k, H,
+    st = lib.fp8q_moe_combine(o.data_ptr(), ldo, plan.pos.data_ptr(), weights.data_ptr(), T, k, H,
                               y.data_ptr(), ldy, _launch_stream(stream, o, weights, y, plan.pos))
     _check("fp8q_moe_combine", st)
     return y
