@@ -160,8 +160,9 @@ __device__ __forceinline__ uint32_t fp4_code1(float y, const Fp4Scale& s) {
 // fp32 silu(g) u: e = 2^(-g log2 e) by ex2.approx of the rounded product plus
 // its exact residual (first order), one rounding of 1 + e, a division good to
 // 2 ulp and a product: relative error below 2^-20 for |g| <= 85.  Beyond, e over- or
-// underflows: g / inf = -0 and g / 1 are the limits.  The residual term is
-// dropped there (0 inf would be NaN).
+// underflows: g / inf = -0 and g / 1 are the limits (below -85 silu itself is less
+// than 2^-116, below -87.3, where __fdividef gives 0, less than 2^-119).  The
+// residual term is dropped there (0 inf would be NaN).
 __device__ __forceinline__ float silu_mul_f32(float g, float u) {
   const float L2E = 1.44269502f;           // fl32(log2 e)
   const float L2E_LO = 1.925963e-8f;       // log2 e - L2E

@@ -36,9 +36,15 @@ extern "C" {
  *           g must be positive, between 2^-64 and 2^64.
  *   mxfp4   groups of 32, value = code * sf: sf = fl32(max(amax, 1e-10) / 6)
  *           rounded up to a power of two, stored as its E8M0 byte (254 at
- *           most); no tensor scale (`gscale` must be NULL)
+ *           most); no tensor scale (`gscale` must be NULL).  The OCP MX rule,
+ *           2^(floor(log2 amax) - 2), lets the largest values saturate: for an
+ *           amax above 1.5 times the power of two below it, its byte is one less
+ *           than this one, else (from 1e-10 on) the same.  Both are mxfp4
+ *           tensors, and the products take either.
  * Codes go to the nearest, ties to the even code, saturating at +-6; every
- * code keeps its value's sign.  NaN inputs are unspecified.
+ * code keeps its value's sign.  A y that is NaN (a NaN input, 0 times
+ * infinity, a gate of -infinity, a row of zeros under eps = 0) leaves the codes
+ * and the scale of its group unspecified.
  *   codes   two to a byte, the lower index in the low half; K must be a
  *           multiple of 32
  *   scales  bytes in blocks of 128 rows x 4 groups, the layout the tensor core
@@ -114,14 +120,18 @@ FP8Q_API fp8q_status fp8q_scaled_mm_fp4(const void* a_q, const void* b_q, const 
  *            equal groups of neighbours; a group counts with its largest key,
  *            or, with a bias, the sum of its two largest; experts outside the
  *            best topk_groups groups are not selected
- *   ids      the topk largest keys, descending, as fp64 tells them apart; equal
- *            keys (and equal groups) go to the lowest index
+ *   ids      the topk largest keys, descending; equal keys (and equal groups)
+ *            go to the lowest index.  With a bias keys are as fp64 tells them
+ *            apart; without one the logits decide, with which both scores grow
+ *            (scores that fp64 rounds to the same value are not equal then)
  *   weights  the scores of the selected experts, divided by their sum if
  *            renormalize is set (0 where that sum is 0), times scale
  * Scores are those of fp64 (smaller ones count as 0), each good to 2^-19 of
  * itself; an fp32 weight below 2^-126 may be 0.
- * A logit of -inf (or NaN) masks its expert: score 0, selected only after all
- * unmasked ones; a token whose experts are all masked has weights 0.
+ * A logit of -inf (or NaN) masks its expert: score 0, key -inf, selected only
+ * after all unmasked ones of the groups that are left; a token whose experts are
+ * all masked has weights 0.  A sum with a masked key is -inf, too: with a bias
+ * a group with one unmasked expert counts no more than one with none.
  *   E <= 512, topk <= 32, num_groups <= 32 (else FP8Q_ERR_UNSUPPORTED);
  *   topk <= E / num_groups * topk_groups
  *   weights fp32 [T, topk], ids int32 [T, topk], both contiguous
@@ -134,8 +144,9 @@ FP8Q_API fp8q_status fp8q_moe_route(const void* logits, int logits_bf16, int64_t
 /*
  * fp8q_moe_plan -- order n = T topk (token, slot) entries by expert, in entry
  * order within an expert.
- *   ids         int32 [n]; an id outside [0, E) gets no row (an expert that
- *               another GPU holds)
+ *   ids         int32 [n]; any id outside [0, E), negative ones of every size
+ *               among them, gets no row (an expert that another GPU holds; the
+ *               ids may be given less the first expert that is here)
  *   offsets     int32 [E + 1]: expert e's rows are [offsets[e], offsets[e+1])
  *   sf_offsets  int32 [E + 1]: its scales begin at block row sf_offsets[e]
  *               (every expert begins a block row of its own; n rows of E
@@ -182,8 +193,9 @@ FP8Q_API fp8q_status fp8q_grouped_mm_fp4(const void* a_q, const void* b_q, const
  * fp8q_grouped_mm_fp4_silu_quant -- the experts' gate_up product with SiLU*mul
  * and the next quantization in its epilogue.  b_q [E, 2I, K] = [gate | up];
  * h = ga gb a b^T stays fp32, y = silu(h_gate) h_up (fp32, not rounded to
- * bf16), then codes q [M, I] (I / 2 bytes a row) and scales sf at the same
- * rows and scale rows as the input, with tensor scale gscale.
+ * bf16; silu good to 2^-20 of itself for gates of at least -85, below to 2^-119),
+ * then codes q [M, I] (I / 2 bytes a row) and scales sf at the same rows and
+ * scale rows as the input, with tensor scale gscale.
  * I must be a multiple of 128 (else FP8Q_ERR_UNSUPPORTED; pad with zero rows).
  */
 FP8Q_API fp8q_status fp8q_grouped_mm_fp4_silu_quant(const void* a_q, const void* b_q, const uint8_t* a_sf,
